@@ -40,6 +40,9 @@ Parity status per function:
   optim (stateful sketch update rules): "parity unpinned" - the pages name
       stateful sketch optimizers without defining one; the textbook momentum
       and Adam rules used here are pinned against closed forms only.
+  logprob, adamw, adapter (the operators around the sketch in a policy step):
+      textbook definitions, pinned against closed forms and differences.
 """
 
 from . import bf16, philox, projection, sketch, merge, kl, optim  # noqa: F401
+from . import logprob, adamw, adapter  # noqa: F401

@@ -14,4 +14,7 @@ from .api import (GAUSSIAN, MAX_SHARED, MAX_SWEEP, RADEMACHER, SKETCH_OVERWRITE,
                   merge_many, sketch_shared_ws_bytes, sketch_update, sketch_ws_bytes, sketch_workspace,
                   sketch_p_bytes, sketch_project, sketch_project_ws_bytes, sketch_accumulate_p,
                   sketch_accumulate_p_ws_bytes)
+from .policy import (MAX_TOP, STATE_BLOCK, TokenLogprob, adamw_bind,  # noqa: F401
+                     adamw_state_values, adamw_step, adapter_apply, adapter_ws_bytes,
+                     token_logprob, token_logprob_backward, token_logprob_ws_bytes)
 from . import sync  # noqa: F401,E402

@@ -11,6 +11,7 @@ import re
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "liblogra.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "logra.h")
+POLICY_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "logra_policy.h")
 
 _lib = None
 
@@ -108,6 +109,34 @@ SIGNATURES.update({
                                                  ctypes.POINTER(ctypes.c_int64),
                                                  ctypes.POINTER(c_vp), c_vp, ctypes.c_size_t,
                                                  c_vp]),
+})
+
+
+class AdamWItem(ctypes.Structure):
+    """logra_adamw_item of include/logra_policy.h (field for field)."""
+    _fields_ = [("p", c_vp), ("g", c_vp), ("master", c_vp), ("m", c_vp), ("v", c_vp),
+                ("m_exp", c_vp), ("v_exp", c_vp), ("n", ctypes.c_int64),
+                ("weight_decay", ctypes.c_float), ("p_type", ctypes.c_int32),
+                ("g_type", ctypes.c_int32)]
+
+
+_i32, _i64, _f32, _f64, _sz = (ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_double,
+                               ctypes.c_size_t)
+# include/logra_policy.h
+SIGNATURES.update({
+    "logra_token_logprob_ws_bytes": (_sz, [_i64, _i64, _i32]),
+    "logra_token_logprob": (ctypes.c_int, [c_vp, ctypes.c_int, _i64, _i64, _i64, c_vp, _f32, _i32,
+                                           c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, _sz, c_vp]),
+    "logra_token_logprob_backward": (ctypes.c_int, [c_vp, ctypes.c_int, _i64, _i64, _i64, c_vp,
+                                                    _f32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, _i64,
+                                                    c_vp]),
+    "logra_adamw_step": (ctypes.c_int, [_i32, ctypes.POINTER(AdamWItem), _f64, _f64, _f64, _f64,
+                                        _i64, c_vp, c_vp]),
+    "logra_adamw_state_values": (ctypes.c_int, [ctypes.c_int, c_vp, c_vp, _i64, c_vp, c_vp]),
+    "logra_adapter_ws_bytes": (_sz, [_i64, _i64, _i64, _i32]),
+    "logra_adapter_apply": (ctypes.c_int, [c_vp, _i64, c_vp, _i64, c_vp, _i64, _i64, _i64, _i64,
+                                           _i32, _i64, c_vp, c_vp, ctypes.c_int, c_vp, c_vp, _i64,
+                                           c_vp, c_vp, _sz, c_vp]),
 })
 
 OK, EINVAL, EWORKSPACE, EHIP = 0, -1, -2, -3

@@ -20,7 +20,8 @@ CALIB_LIB = os.path.join(PKG, "liblogra_calib.so")   # measurement helper (a pla
 ARCH = "gfx950"
 
 SOURCES = ["abi.cpp", "regen.hip", "sketch.hip", "merge.hip", "kl.hip", "kl_sweep.hip", "optim.hip",
-           "noalloc.hip"]
+           "noalloc.hip", "policy/abi_policy.cpp", "policy/logprob.hip", "policy/adamw.hip",
+           "policy/adapter.hip"]
 
 
 def hipcc():
@@ -39,7 +40,7 @@ def common_flags():
 
 
 def _compile(src):
-    obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
+    obj = os.path.join(BUILD, os.path.splitext(os.path.basename(src))[0] + ".o")
     cmd = [hipcc(), *common_flags(), "-c", os.path.join(CSRC, src), "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:

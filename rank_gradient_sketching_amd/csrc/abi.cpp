@@ -13,12 +13,23 @@ namespace {
 
 thread_local char g_hip_msg[256] = "";
 
+}  // namespace
+
+namespace logra {
+
+// Status of a HIP call; its text is kept for logra_status_str.
 int hip_status(hipError_t e) {
   if (e == hipSuccess) return LOGRA_OK;
   snprintf(g_hip_msg, sizeof(g_hip_msg), "HIP error %d: %s", (int)e,
            hipGetErrorString(e));
   return LOGRA_EHIP;
 }
+
+}  // namespace logra
+
+namespace {
+
+using logra::hip_status;
 
 bool aligned(const void* p, uintptr_t a) {
   return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;

@@ -10,6 +10,9 @@ namespace logra {
 
 inline int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 
+// Status of a HIP call, its text kept for logra_status_str (abi.cpp).
+int hip_status(hipError_t e);
+
 // Projections that share the layer input X (and so, with the same seed, the
 // same A) can be sketched together: one projection pass, one accumulate
 // launch over all of their d groups.  A call takes up to kMaxGroups such input

@@ -1,0 +1,404 @@
+// logra_adamw_step: one AdamW step over many tensors, states in fp32 or in 8
+// bits, on gfx950; logra_adamw_state_values: 8-bit states as values.
+//
+// Mathematics (per entry, fp32):
+//   m' = b1 m + (1 - b1) g,   v' = b2 v + (1 - b2) g^2,
+//   w' = w - lr ((m' / bc1) / (sqrt(v' / bc2) + eps) + wd w),
+// written with r = sqrt(v'): sqrt(v' / bc2) = r / sqrt(bc2), so the 8-bit form,
+// which holds r, needs no second root.
+//
+// The 8-bit form (include/logra_policy.h has its bits): 32 entries share an
+// exponent byte, an entry is a small float below the block's largest, so
+// decoding is a shift and an add on the fp32 pattern and no table is read.
+// r is held instead of v because it needs half the binades.  Rounding adds a
+// dither from a counter and truncates: rounded to nearest, v with beta2 =
+// 0.999 would never move (the root changes by at most 0.05 % a step, the
+// spacing is 3 to 6 %) - simulated over 6000 steps of unit-variance gradients,
+// sqrt(v) then ended at 0.52 of its true value, and with the dither at 1.00
+// with a spread of 0.09 (the counter's equally spaced dithers; 0.10 with
+// random ones).  The m of a block share the 32 lanes' maximum by three
+// cross-lane steps (four entries per lane, eight lanes per block).
+//
+// Bound: HBM bytes (a bf16 weight with fp32 master, bf16 gradient and fp32
+// states moves 28 bytes an entry, 8-bit states 16).  A work-group takes 4096
+// consecutive entries of one tensor, every load of its four steps issued
+// before the first is used.  The tensors of a launch travel in its argument
+// block (48 at most), where a work-group finds its own by comparing all
+// tensors' first chunks at once, one per lane.
+#include <math.h>
+
+#include <type_traits>
+
+#include "common.hpp"
+#include "internal.hpp"
+#include "policy/internal_policy.hpp"
+
+namespace logra {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVec = 4;                              // entries per lane and step
+constexpr int kSteps = 4;
+constexpr int kChunk = kThreads * kVec * kSteps;     // entries per work-group
+constexpr int kMaxItems = 48;
+
+struct Item {
+  void* p;
+  const void* g;
+  float* master;
+  void* m;
+  void* v;
+  uint8_t* m_exp;
+  uint8_t* v_exp;
+  int64_t n;
+  float weight_decay;
+  uint32_t dither0;
+  int vec;      // every array on a boundary of kVec of its entries
+  int pad;
+};
+struct Launch {
+  AdamwScalars h;
+  int n;
+  int first[kMaxItems];   // first work-group of each tensor
+  Item item[kMaxItems];
+};
+static_assert(sizeof(Launch) <= 4096, "kernel argument block");
+
+// ---------------------------------------------------------------- 8-bit states
+constexpr int kKeepM = 3, kKeepV = 4;            // mantissa bits kept
+constexpr int kExpMin = 16, kExpNan = 255;
+
+template <int KEEP>
+__device__ __forceinline__ float decode(uint32_t c, int E) {
+  const uint32_t b = ((uint32_t)(E - 15) << 23) + (c << (23 - KEEP));
+  const float x = c ? __uint_as_float(b) : 0.0f;
+  return E == kExpNan ? NAN : x;
+}
+__device__ __forceinline__ float decode_m(uint32_t code, int E) {
+  const float x = decode<kKeepM>(code & 127u, E);
+  return (code & 128u) ? -x : x;
+}
+
+// Largest value over the eight lanes that hold a block.
+__device__ __forceinline__ int block_max(int x) {
+  // lanes 1 and 2 apart inside a quad, then the other quad of the half row
+  x = max(x, __builtin_amdgcn_mov_dpp(x, 0xB1, 0xF, 0xF, true));    // quad_perm [1,0,3,2]
+  x = max(x, __builtin_amdgcn_mov_dpp(x, 0x4E, 0xF, 0xF, true));    // quad_perm [2,3,0,1]
+  x = max(x, __builtin_amdgcn_mov_dpp(x, 0x141, 0xF, 0xF, true));   // row_half_mirror
+  return x;
+}
+
+// Codes of the magnitudes x (>= 0 or NaN) of a lane's entries: packed bytes,
+// and the block's exponent.  `least`: a nonzero x keeps a nonzero code.
+template <int KEEP>
+__device__ __forceinline__ uint32_t encode(const float* x, uint32_t h0, bool least, int* E_out) {
+  uint32_t t[kVec];
+  int top = 0;
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) {
+    t[e] = __float_as_uint(x[e]) + ((h0 + (uint32_t)e * kDitherIndex) >> (9 + KEEP));
+    top = max(top, (int)(t[e] >> 23));
+  }
+  const int E = min(max(block_max(top), kExpMin), kExpNan);
+  const int base = (E - 15) << KEEP;
+  uint32_t packed = 0;
+#pragma unroll
+  for (int e = 0; e < kVec; ++e) {
+    int c = (int)(t[e] >> (23 - KEEP)) - base;
+    c = max(c, least && x[e] > 0.0f ? 1 : 0);
+    packed |= (uint32_t)min(c, KEEP == kKeepM ? 127 : 255) << (8 * e);
+  }
+  *E_out = E;
+  return packed;
+}
+
+// ---------------------------------------------------------------- arrays
+// Entries i .. i + 3 of an array (`vec`: one aligned load; else each on its
+// own, entries past n not touched).
+template <class F>
+__device__ __forceinline__ void each(int64_t i, int64_t n, F f) {
+#pragma unroll
+  for (int e = 0; e < kVec; ++e)
+    if (i + e < n) f(e);
+}
+__device__ __forceinline__ void load4(const float* a, int64_t i, int64_t n, bool vec, float* x) {
+  if (vec) {
+    const f32x4 q = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(a + i));
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) x[e] = q[e];
+  } else {
+    each(i, n, [&](int e) { x[e] = a[i + e]; });
+  }
+}
+__device__ __forceinline__ void load4(const uint16_t* a, int64_t i, int64_t n, bool vec, float* x) {
+  if (vec) {
+    const u32x2 q = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(a + i));
+    x[0] = bf16_lo(q[0]);
+    x[1] = bf16_hi(q[0]);
+    x[2] = bf16_lo(q[1]);
+    x[3] = bf16_hi(q[1]);
+  } else {
+    each(i, n, [&](int e) { x[e] = bf16_to_f32(a[i + e]); });
+  }
+}
+__device__ __forceinline__ uint32_t load4(const uint8_t* a, int64_t i, int64_t n, bool vec) {
+  if (vec) return __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(a + i));
+  uint32_t q = 0;
+  each(i, n, [&](int e) { q |= (uint32_t)a[i + e] << (8 * e); });
+  return q;
+}
+__device__ __forceinline__ void store4(float* a, int64_t i, int64_t n, bool vec, const float* x) {
+  if (vec) {
+    const f32x4 q = {x[0], x[1], x[2], x[3]};
+    __builtin_nontemporal_store(q, reinterpret_cast<f32x4*>(a + i));
+  } else {
+    each(i, n, [&](int e) { a[i + e] = x[e]; });
+  }
+}
+__device__ __forceinline__ void store4(uint16_t* a, int64_t i, int64_t n, bool vec,
+                                       const float* x) {
+  if (vec) {
+    const u32x2 q = {pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3])};
+    __builtin_nontemporal_store(q, reinterpret_cast<u32x2*>(a + i));
+  } else {
+    each(i, n, [&](int e) { a[i + e] = f32_to_bf16(x[e]); });
+  }
+}
+__device__ __forceinline__ void store4(uint8_t* a, int64_t i, int64_t n, bool vec, uint32_t q) {
+  if (vec) {
+    __builtin_nontemporal_store(q, reinterpret_cast<uint32_t*>(a + i));
+  } else {
+    each(i, n, [&](int e) { a[i + e] = (uint8_t)(q >> (8 * e)); });
+  }
+}
+
+// ---------------------------------------------------------------- the step
+template <AdamwWeights W, bool G32, bool S8>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(const Launch L) {
+  typedef typename std::conditional<W == AdamwWeights::kF32, float, uint16_t>::type PT;
+  typedef typename std::conditional<G32, float, uint16_t>::type GT;
+  const int lane = threadIdx.x & 63;
+  const int wg = (int)blockIdx.x;
+  const int mine = lane < L.n && L.first[lane < kMaxItems ? lane : 0] <= wg;
+  const int it = __builtin_amdgcn_readfirstlane(__popcll(__ballot(mine)) - 1);
+  PT* const p = static_cast<PT*>(L.item[it].p);
+  const GT* const g = static_cast<const GT*>(L.item[it].g);
+  float* const master = L.item[it].master;
+  void* const mp = L.item[it].m;
+  void* const vp = L.item[it].v;
+  uint8_t* const m_exp = L.item[it].m_exp;
+  uint8_t* const v_exp = L.item[it].v_exp;
+  const int64_t n = L.item[it].n;
+  const float wd = L.item[it].weight_decay;
+  const uint32_t d0 = L.item[it].dither0;
+  const bool vec_ok = L.item[it].vec != 0;
+  const float lr = L.h.lr, b1 = L.h.b1, b2 = L.h.b2, c1 = L.h.c1, c2 = L.h.c2, eps = L.h.eps;
+  const float ibc1 = L.h.inv_bc1, isbc2 = L.h.inv_sqrt_bc2;
+  const uint32_t dstep = L.h.dither_step;
+  const float gs = L.h.grad_scale ? *L.h.grad_scale : 1.0f;
+
+  const int64_t i0 = (int64_t)(wg - L.first[it]) * kChunk + (int64_t)threadIdx.x * kVec;
+  float xw[kSteps][kVec], xg[kSteps][kVec], xm[kSteps][kVec], xv[kSteps][kVec];
+  uint32_t qm[kSteps], qv[kSteps];
+  int em[kSteps], ev[kSteps];
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const int64_t i = i0 + (int64_t)s * kThreads * kVec;
+    const bool vec = vec_ok && i + kVec <= n;
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) xw[s][e] = xg[s][e] = xm[s][e] = xv[s][e] = 0.0f;
+    qm[s] = qv[s] = 0;
+    em[s] = ev[s] = kExpMin;
+    if (i < n) {
+      if constexpr (W == AdamwWeights::kBf16Master)
+        load4(master, i, n, vec, xw[s]);
+      else
+        load4(p, i, n, vec, xw[s]);
+      load4(g, i, n, vec, xg[s]);
+      if constexpr (S8) {
+        qm[s] = load4(static_cast<const uint8_t*>(mp), i, n, vec);
+        qv[s] = load4(static_cast<const uint8_t*>(vp), i, n, vec);
+        em[s] = m_exp[i / kStateBlock];
+        ev[s] = v_exp[i / kStateBlock];
+      } else {
+        load4(static_cast<const float*>(mp), i, n, vec, xm[s]);
+        load4(static_cast<const float*>(vp), i, n, vec, xv[s]);
+      }
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < kSteps; ++s) {
+    const int64_t i = i0 + (int64_t)s * kThreads * kVec;
+    const bool vec = vec_ok && i + kVec <= n;
+    float xr[kVec];
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      if constexpr (S8) {
+        xm[s][e] = decode_m((qm[s] >> (8 * e)) & 255u, em[s]);
+        const float r = decode<kKeepV>((qv[s] >> (8 * e)) & 255u, ev[s]);
+        xv[s][e] = r * r;
+      }
+      const float gr = xg[s][e] * gs;
+      const float m = fmaf(b1, xm[s][e], c1 * gr);
+      const float v = fmaf(b2, xv[s][e], c2 * gr * gr);
+      const float r = sqrtf(v);
+      const float step = (m * ibc1) / fmaf(r, isbc2, eps);
+      xw[s][e] = xw[s][e] - lr * fmaf(wd, xw[s][e], step);
+      xm[s][e] = m;
+      xv[s][e] = v;
+      xr[e] = r;
+    }
+    if constexpr (S8) {
+      // (entries past n are zeros here; every lane takes part in the block's
+      // maximum)
+      const uint32_t h = (d0 + (uint32_t)i) * kDitherIndex + dstep;
+      float xa[kVec];
+      uint32_t sign = 0;
+#pragma unroll
+      for (int e = 0; e < kVec; ++e) {
+        xa[e] = fabsf(xm[s][e]);
+        sign |= (__float_as_uint(xm[s][e]) >> 31) << (8 * e + 7);
+        if (i + e >= n) xa[e] = xr[e] = 0.0f;
+      }
+      int E;
+      const uint32_t cm = encode<kKeepM>(xa, h, false, &E) | sign;
+      em[s] = E;
+      const uint32_t cv = encode<kKeepV>(xr, h + 0x80000000u, true, &E);
+      ev[s] = E;
+      qm[s] = cm;
+      qv[s] = cv;
+    }
+    if (i < n) {
+      store4(p, i, n, vec, xw[s]);
+      if constexpr (W == AdamwWeights::kBf16Master) store4(master, i, n, vec, xw[s]);
+      if constexpr (S8) {
+        store4(static_cast<uint8_t*>(mp), i, n, vec, qm[s]);
+        store4(static_cast<uint8_t*>(vp), i, n, vec, qv[s]);
+        if ((lane & 7) == 0) {
+          m_exp[i / kStateBlock] = (uint8_t)em[s];
+          v_exp[i / kStateBlock] = (uint8_t)ev[s];
+        }
+      } else {
+        store4(static_cast<float*>(mp), i, n, vec, xm[s]);
+        store4(static_cast<float*>(vp), i, n, vec, xv[s]);
+      }
+    }
+  }
+}
+
+template <bool SECOND>
+__global__ __launch_bounds__(kThreads) void state_values_kernel(const uint8_t* __restrict__ codes,
+                                                                const uint8_t* __restrict__ exps,
+                                                                int64_t n, bool vec_ok,
+                                                                uint16_t* __restrict__ out) {
+  const int64_t stride = (int64_t)gridDim.x * kThreads * kVec;
+  for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * kVec; i < n; i += stride) {
+    const bool vec = vec_ok && i + kVec <= n;
+    const uint32_t q = load4(codes, i, n, vec);
+    const int E = exps[i / kStateBlock];
+    float x[kVec];
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) {
+      const uint32_t c = (q >> (8 * e)) & 255u;
+      x[e] = SECOND ? decode<kKeepV>(c, E) : decode_m(c, E);
+    }
+    store4(out, i, n, vec, x);
+  }
+}
+
+bool on(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+template <AdamwWeights W, bool G32, bool S8>
+hipError_t launch_variant(const AdamwItem* const* items, int n, const AdamwScalars& h,
+                          hipStream_t s) {
+  constexpr int64_t kMostGroups = (int64_t(1) << 24) - 1;   // 2^32 threads less one group
+  Launch L;
+  L.h = h;
+  L.n = 0;
+  int64_t groups = 0;
+  auto flush = [&]() {
+    if (L.n == 0) return hipSuccess;
+    hipLaunchKernelGGL((adamw_kernel<W, G32, S8>), dim3((unsigned)groups), dim3(kThreads), 0, s, L);
+    L.n = 0;
+    groups = 0;
+    return hipGetLastError();
+  };
+  for (int i = 0; i < n; ++i) {
+    AdamwItem q = *items[i];
+    // a tensor past one launch's work-groups goes on in the next, at a whole
+    // number of chunks (so of blocks)
+    while (q.n > 0) {
+      const int64_t chunks = (q.n + kChunk - 1) / kChunk;
+      const int64_t room = kMostGroups - groups;
+      if (L.n == kMaxItems || room == 0) {
+        const hipError_t e = flush();
+        if (e != hipSuccess) return e;
+        continue;
+      }
+      const int64_t take = chunks <= room ? q.n : room * kChunk;
+      const size_t pb = W == AdamwWeights::kF32 ? 4 : 2, gb = G32 ? 4 : 2, sb = S8 ? 1 : 4;
+      L.first[L.n] = (int)groups;
+      L.item[L.n] = Item{q.p, q.g, q.master, q.m, q.v, q.m_exp, q.v_exp, take, q.weight_decay,
+                         q.dither0,
+                         on(q.p, kVec * pb) && on(q.g, kVec * gb) && on(q.master, kVec * 4) &&
+                                 on(q.m, kVec * sb) && on(q.v, kVec * sb)
+                             ? 1
+                             : 0,
+                         0};
+      ++L.n;
+      groups += (take + kChunk - 1) / kChunk;
+      q.p = static_cast<char*>(q.p) + take * pb;
+      q.g = static_cast<const char*>(q.g) + take * gb;
+      if (q.master) q.master += take;
+      q.m = static_cast<char*>(q.m) + take * sb;
+      q.v = static_cast<char*>(q.v) + take * sb;
+      if (S8) {
+        q.m_exp += take / kStateBlock;
+        q.v_exp += take / kStateBlock;
+      }
+      q.dither0 += (uint32_t)take;
+      q.n -= take;
+    }
+  }
+  return flush();
+}
+
+template <AdamwWeights W>
+hipError_t launch_weights(bool g_f32, bool state8, const AdamwItem* const* items, int n,
+                          const AdamwScalars& h, hipStream_t s) {
+  if (g_f32)
+    return state8 ? launch_variant<W, true, true>(items, n, h, s)
+                  : launch_variant<W, true, false>(items, n, h, s);
+  return state8 ? launch_variant<W, false, true>(items, n, h, s)
+                : launch_variant<W, false, false>(items, n, h, s);
+}
+
+}  // namespace
+
+hipError_t launch_adamw(AdamwWeights weights, bool g_f32, bool state8,
+                        const AdamwItem* const* items, int n, const AdamwScalars& h,
+                        hipStream_t s) {
+  switch (weights) {
+    case AdamwWeights::kF32: return launch_weights<AdamwWeights::kF32>(g_f32, state8, items, n, h, s);
+    case AdamwWeights::kBf16:
+      return launch_weights<AdamwWeights::kBf16>(g_f32, state8, items, n, h, s);
+    default: return launch_weights<AdamwWeights::kBf16Master>(g_f32, state8, items, n, h, s);
+  }
+}
+
+hipError_t launch_adamw_state_values(bool second, const uint8_t* codes, const uint8_t* exps,
+                                     int64_t n, uint16_t* out, hipStream_t s) {
+  int64_t blocks = (n + kThreads * kVec - 1) / (kThreads * kVec);
+  if (blocks > (1 << 20)) blocks = 1 << 20;
+  const bool vec = on(codes, kVec) && on(out, 2 * kVec);
+  if (second)
+    hipLaunchKernelGGL((state_values_kernel<true>), dim3((unsigned)blocks), dim3(kThreads), 0, s,
+                       codes, exps, n, vec, out);
+  else
+    hipLaunchKernelGGL((state_values_kernel<false>), dim3((unsigned)blocks), dim3(kThreads), 0, s,
+                       codes, exps, n, vec, out);
+  return hipGetLastError();
+}
+
+}  // namespace logra
