@@ -10,33 +10,32 @@
 // Two launches:
 //   project  P = X A^T, fp32, for 32 rows and a piece of k per work-group.  The
 //            rank is the MFMA's row index and the tokens its columns, so a
-//            token's values lie in the lanes of its own column and the rows of
-//            a tile that belong to other policies (or hold NaN) touch nothing.
-//            A tile's policies are found by ballots and taken one after the
-//            other, or dealt to several work-groups where few tiles leave the
-//            chip empty; each writes the P of its own rows.  Signs: one Philox
-//            block per thread gives 256 rows x 256 columns' worth at a time
-//            (rows x chunks), kept in LDS and expanded to +-1 in registers, so
-//            a seeded A is never read: a decoding batch over many policies
-//            streams only U.
-//   expand   out = Y + P U^T for 64 rows (16 for few rows) x 64 columns per
-//            wave.  U's rows are the MFMA's rows, in the order that leaves each
-//            lane 16 consecutive columns of one token.  P (its pieces summed in
-//            order and scaled) and fp32 U enter as bf16 pairs hi + lo of 16
-//            significant bits; lo x lo, 2^-16 of the product, is left out.  The
-//            rows of each policy are written as soon as it is done; rows with
-//            none are copied.
+//            token's values lie in the lanes of its own column and rows of other
+//            policies (or holding NaN) touch nothing.  A tile's policies are
+//            found by ballots; few tiles deal them to several work-groups.
+//            Signs are drawn and expanded to +-1 in registers, so a seeded A is
+//            never read: a decoding batch over many policies streams only U.
+//   expand   out = Y + P U^T in blocks of 16 rows x 64 columns per wave, U's rows
+//            as the MFMA's rows.  P (its pieces summed in order and scaled) and
+//            fp32 U enter as bf16 pairs hi + lo of 16 significant bits; lo x lo,
+//            2^-16 of the product, is left out.  Few blocks: one wave each
+//            (adapter_block_kernel).  Many: waves walk down several with U in
+//            registers (adapter_rows_kernel) or in LDS (adapter_strip_kernel).
 // Bound: X and Y once in, out once (prompts); U of every policy in use, and
 // launch latency (single tokens).
+#include <type_traits>
+
 #include "common.hpp"
 #include "internal.hpp"
 #include "policy/internal_policy.hpp"
+
+// (a lambda that is not inlined would hold its captures in scratch memory)
+#define LOGRA_INLINE __attribute__((always_inline))
 
 namespace logra {
 
 namespace {
 
-constexpr int kThreads = 256;
 constexpr int kTileRows = 32;      // rows of a projection tile
 constexpr int kChunk = 256;        // columns of a sign block
 
@@ -60,40 +59,36 @@ struct Policies {
   }
 };
 
-// Elements col .. col + 7 of a bf16 row of n, those past n as zeros (and not
-// read: the last row of a matrix need not have padding behind it).
-__device__ __forceinline__ u32x4 load_row8(const uint16_t* row, int col, int n) {
-  if (col + 8 <= n) return load_bf16x8(row, col);
-  u32x4 v = {0, 0, 0, 0};
-#pragma unroll
-  for (int e = 0; e < 8; ++e)
-    if (col + e < n) v[e >> 1] |= (uint32_t)row[col + e] << (16 * (e & 1));
-  return v;
-}
-
 // ---------------------------------------------------------------- project
-// NB 16-row blocks of A: per wave kNbw of them, kKsub waves sharing a block and
-// splitting its steps of 32 columns.
+// One work-group: kTileRows rows and a piece of k.  Its waves take 256-column
+// chunks in turn and each multiplies its own with all of r, so the main loop has
+// no barrier; their sums meet in LDS at the end, in order.  A chunk reaches LDS
+// as two halves of 128 columns by direct global->LDS copies of whole cache lines
+// (4 rows x 256 bytes an instruction), one half in flight while the other is
+// multiplied; 16-byte piece j of row t lies at slot j ^ (t % 16) against bank
+// conflicts.  In step s of a half, lanes 0-31 / 32-63 carry its columns 8 s ..
+// / 64 + 8 s ..: byte s of one of the sign block's four words.
+constexpr int kHalfCols = 128;
+constexpr int kHalfBytes = kTileRows * kHalfCols * 2;
+constexpr int kRedRow = 36;   // floats of a token's 32 partial sums in LDS
+constexpr int proj_waves(int nb) { return nb <= 4 ? 8 : 4; }
+
+// NB 32-row blocks of A.
 template <int NB, bool GIVEN>
-__global__ __launch_bounds__(kThreads) void adapter_project_kernel(AdapterArgs a, int n_split,
-                                                                   int chunks_per_split, int n_deal,
-                                                                   float* __restrict__ P) {
-  constexpr int RP = 16 * NB;
-  constexpr int kGroups = NB < 4 ? NB : 4;
-  constexpr int kKsub = 4 / kGroups;
-  constexpr int kNbw = NB / kGroups;
-  constexpr int kSuper = 256 / RP;          // chunks whose signs fit one pass
-  constexpr int kRowBytes = kChunk * 2;
-  __shared__ __attribute__((aligned(16))) unsigned char xs[kTileRows * kRowBytes];
-  __shared__ uint64_t sgn[GIVEN ? 1 : 256 * 4];
-  __shared__ f32x4 red[kKsub > 1 ? 4 * 2 * kNbw * 64 : 1];
+__global__ __launch_bounds__(64 * proj_waves(NB)) void adapter_project_kernel(
+    AdapterArgs a, int rp, int n_split, int chunks_per_split, int n_deal, float* __restrict__ P) {
+  constexpr int W = proj_waves(NB);
+  constexpr int kStepsAtOnce = NB >= 4 ? 2 : 4;   // (more at once spilled registers)
+  __shared__ __attribute__((aligned(16))) unsigned char stage[2][W][kHalfBytes];
+  static_assert(W * kTileRows * kRedRow * 4 <= sizeof(stage), "partial sums fit");
   const int tid = threadIdx.x;
   const int lane = tid & 63;
   const int wave = tid >> 6;
-  const int m = lane & 15;    // row of A in its block; token in its block
-  const int g = lane >> 4;    // 64-column quarter of a chunk
-  const int grp = wave / kKsub, ksub = wave % kKsub;
+  const int m = lane & 31;    // row of A in its block; token
+  const int h = lane >> 5;
   const SignMasks smk = sign_masks();
+  unsigned char* const buf0 = stage[0][wave];
+  unsigned char* const buf1 = stage[1][wave];
 
   const int n_tiles = (int)((a.T + kTileRows - 1) / kTileRows);
   const int tile = (int)(blockIdx.x % n_tiles);
@@ -101,128 +96,211 @@ __global__ __launch_bounds__(kThreads) void adapter_project_kernel(AdapterArgs a
   const int split = rest % n_split;
   const int deal = rest / n_split;
   const int64_t t0 = (int64_t)tile * kTileRows;
-  const int n_chunks = (a.k + kChunk - 1) / kChunk;
+  const int all_chunks = (a.k + kChunk - 1) / kChunk;
   const int ch0 = split * chunks_per_split;
-  const int ch1 = ch0 + chunks_per_split < n_chunks ? ch0 + chunks_per_split : n_chunks;
+  const int n_chunks = min(chunks_per_split, all_chunks - ch0);
+  // work-groups start at different chunks: in step they would all read the same
+  // byte range of their rows, and so the same HBM channels
+  const int rot = tile % n_chunks;
 
   Policies pol(a.adapter, t0 + lane, lane < kTileRows && t0 + lane < a.T, a.n);
-  int id;
-  uint64_t rows;
-  for (int u = 0; pol.next(&id, &rows); ++u) {
-    if (u % n_deal != deal) continue;
-    uint64_t seed = 0, stream = 0;
-    const uint16_t* A = nullptr;
-    if constexpr (GIVEN) {
-      A = a.A + (int64_t)id * a.r * a.lda;
-    } else {
-      seed = a.seeds[2 * (int64_t)id];
-      stream = a.seeds[2 * (int64_t)id + 1];
-    }
-    f32x4 acc[kNbw][2];
-#pragma unroll
-    for (int b = 0; b < kNbw; ++b)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) acc[b][h] = f32x4{0.f, 0.f, 0.f, 0.f};
 
-    // this thread's four 16-byte pieces of a chunk's X tile
-    u32x4 xr[4];
-    auto fetch = [&](int ch) {
+  f32x16 acc[NB];
+  auto clear = [&]() LOGRA_INLINE {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t t = t0 + (tid >> 5) + 8 * i;
-        const uint16_t* row = a.X + (t < a.T ? t : a.T - 1) * a.ldx;
-        xr[i] = load_row8(row, ch * kChunk + 8 * (tid & 31), a.k);
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) acc[b][v] = 0.0f;
+  };
+  auto phys = [&](int c) LOGRA_INLINE {
+    c += rot;
+    return ch0 + (c < n_chunks ? c : c - n_chunks);
+  };
+  // Rows past T re-read the last one (they belong to no policy); pieces past k
+  // re-read the row's first and are cleared when read back.  (A piece that ends
+  // past k is an aligned 16-byte group that holds an element of the row.)
+  auto issue = [&](int c, int hc, unsigned char* dst) LOGRA_INLINE {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int row = 4 * i + (lane >> 4);
+      const int col = c * kChunk + hc * kHalfCols + 8 * ((lane & 15) ^ (row & 15));
+      const int64_t t = t0 + row < a.T ? t0 + row : a.T - 1;
+      lds_dma16_nt((const void*)(a.X + t * a.ldx + (col < a.k ? col : 0)), lds_addr(dst + i * 1024));
+    }
+  };
+  struct Signs {
+    uint64_t w[NB][2];
+  };
+  Signs sw0, sw1;
+  auto sign_words = [&](int id, int c, Signs& sw) LOGRA_INLINE {
+    const uint64_t seed = a.seeds[2 * (int64_t)id], stream = a.seeds[2 * (int64_t)id + 1];
+    if constexpr (NB == 1) {
+      const Words4 blk = sign_block(seed, stream, (uint64_t)c, (uint64_t)m);
+      sw.w[0][0] = h ? blk.w[1] : blk.w[0];
+      sw.w[0][1] = h ? blk.w[3] : blk.w[2];
+    } else {
+      // lane half h draws the blocks of row block 2 j + h and swaps what the
+      // other half needs
+#pragma unroll
+      for (int j = 0; j < NB / 2; ++j) {
+        const Words4 blk = sign_block(seed, stream, (uint64_t)c, (uint64_t)((2 * j + h) * 32 + m));
+        const uint64_t r0 = swap_halves64(h ? blk.w[0] : blk.w[1]);
+        const uint64_t r2 = swap_halves64(h ? blk.w[2] : blk.w[3]);
+        sw.w[2 * j][0] = h ? r0 : blk.w[0];
+        sw.w[2 * j][1] = h ? r2 : blk.w[2];
+        sw.w[2 * j + 1][0] = h ? blk.w[1] : r0;
+        sw.w[2 * j + 1][1] = h ? blk.w[3] : r2;
+      }
+    }
+  };
+  // One half chunk: A of policy id (signs: the words at hand) against the tokens
+  // with `keep` set (all bits; the others' columns get zeros).
+  auto compute_cols = [&](auto edge, int id, const Signs& sw, uint32_t keep, int c, int hc,
+                          const unsigned char* buf) LOGRA_INLINE {
+    const int col0 = c * kChunk + hc * kHalfCols + 64 * h;
+    const uint16_t* const A = GIVEN ? a.A + (int64_t)id * a.r * a.lda : nullptr;
+#pragma unroll kStepsAtOnce
+    for (int s = 0; s < 8; ++s) {
+      const int slot = (8 * h + s) ^ (m & 15);
+      u32x4 x = *reinterpret_cast<const u32x4*>(buf + m * (kHalfCols * 2) + slot * 16);
+      if constexpr (decltype(edge)::value) x &= keep_mask8(a.k - (col0 + 8 * s));
+      if constexpr (!GIVEN) x &= u32x4{keep, keep, keep, keep};
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        u32x4 w;
+        if constexpr (GIVEN) {
+          const int i = 32 * b + m;
+          w = load_bf16x8_masked(A + (int64_t)(i < a.r ? i : a.r - 1) * a.lda, col0 + 8 * s, a.k);
+        } else {
+          w = signs_to_bf16x8((uint32_t)(sw.w[b][hc] >> (8 * s)) & 0xFFu, smk);
+        }
+        acc[b] = mfma32(w, x, acc[b]);
+      }
+    }
+  };
+  auto compute = [&](int id, const Signs& sw, uint32_t keep, int c, int hc,
+                     const unsigned char* buf) LOGRA_INLINE {
+    if ((c + 1) * kChunk > a.k)     // the chunk that ends past k
+      compute_cols(std::true_type{}, id, sw, keep, c, hc, buf);
+    else
+      compute_cols(std::false_type{}, id, sw, keep, c, hc, buf);
+  };
+  // The rows' whole piece of k, the next half chunk in flight, for all of the
+  // policies dealt to this work-group (signs), or one (given bases).  The words of
+  // the first two are held for both halves; those of others, rare in one tile of a
+  // packed batch, are drawn for each.
+  auto pass = [&](int id0, uint32_t keep0, int id1, uint32_t keep1, const Policies& more_of,
+                  int u_more) LOGRA_INLINE {
+    auto half = [&](int pc, int hc, const unsigned char* buf) LOGRA_INLINE {
+      compute(id0, sw0, keep0, pc, hc, buf);
+      if constexpr (!GIVEN) {
+        if (id1 >= 0) compute(id1, sw1, keep1, pc, hc, buf);
+        Policies q = more_of;
+        int id;
+        uint64_t rows;
+        for (int u = u_more; q.next(&id, &rows); ++u) {
+          if (u % n_deal != deal) continue;
+          Signs sw;
+          sign_words(id, pc, sw);
+          compute(id, sw, ((rows >> m) & 1) ? ~0u : 0u, pc, hc, buf);
+        }
       }
     };
-    if (ch0 < ch1) fetch(ch0);
-    for (int ch = ch0; ch < ch1; ++ch) {
-      __syncthreads();   // xs, sgn and red are free
+    int c = wave;
+    if (c < n_chunks) {
+      issue(phys(c), 0, buf0);
+      issue(phys(c), 1, buf1);
+    }
+    for (; c < n_chunks; c += W) {
+      const int pc = phys(c);
       if constexpr (!GIVEN) {
-        const int sc = (ch - ch0) % kSuper;
-        if (sc == 0) {
-          const int c = ch + tid / RP;
-          if (c < ch1) {
-            const Words4 w = sign_block(seed, stream, (uint64_t)c, (uint64_t)(tid % RP));
-#pragma unroll
-            for (int q = 0; q < 4; ++q) sgn[tid * 4 + q] = w.w[q];
-          }
-        }
+        sign_words(id0, pc, sw0);
+        if (id1 >= 0) sign_words(id1, pc, sw1);
       }
+      const bool more = c + W < n_chunks;
+      vm_wait<8>();          // half 0 is there; half 1's copies may be in flight
+      half(pc, 0, buf0);
+      if (more) {
+        lgkm_wait0();        // this wave has read buf0
+        issue(phys(c + W), 0, buf0);
+        vm_wait<8>();        // half 1 is there
+      } else {
+        vm_wait<0>();
+      }
+      half(pc, 1, buf1);
+      if (more) {
+        lgkm_wait0();
+        issue(phys(c + W), 1, buf1);
+      }
+    }
+    lgkm_wait0();
+  };
+  // Sum of the waves, in order, and P of `rows`; the 2 W threads of a token take
+  // kPer ranks each.
+  auto finish = [&](uint64_t rows) LOGRA_INLINE {
+    constexpr int kPer = 16 / W;
+    float* const red = reinterpret_cast<float*>(&stage[0][0][0]);
+    const int t = tid / (2 * W);
+    const int i0 = (tid % (2 * W)) * kPer;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int row = (tid >> 5) + 8 * i, j = tid & 31;
-        const int slot = (j & 16) | ((j ^ row) & 15);
-        *reinterpret_cast<u32x4*>(xs + row * kRowBytes + slot * 16) = xr[i];
+    for (int b = 0; b < NB; ++b) {
+      __syncthreads();       // every wave is done with what lies there
+#pragma unroll
+      for (int v = 0; v < 16; v += 4) {
+        const f32x4 q = {acc[b][v], acc[b][v + 1], acc[b][v + 2], acc[b][v + 3]};
+        *reinterpret_cast<f32x4*>(red + (wave * kTileRows + m) * kRedRow + 2 * v + 4 * h) = q;
       }
       __syncthreads();
-      if (ch + 1 < ch1) fetch(ch + 1);
-      uint64_t sw[kNbw];
-      if constexpr (!GIVEN) {
+      if (((rows >> t) & 1) && 32 * b + i0 < rp) {
+        float* p = P + ((int64_t)split * a.T + t0 + t) * rp + 32 * b + i0;
 #pragma unroll
-        for (int b = 0; b < kNbw; ++b)
-          sw[b] = sgn[(((ch - ch0) % kSuper) * RP + (grp * kNbw + b) * 16 + m) * 4 + g];
-      }
+        for (int e = 0; e < kPer; ++e) {
+          float sum = red[t * kRedRow + i0 + e];
 #pragma unroll
-      for (int ss = 0; ss < 8 / kKsub; ++ss) {
-        const int s = ss * kKsub + ksub;
-        const int j = 8 * g + s;
-        u32x4 x[2];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const int row = 16 * h + m;
-          const int slot = (j & 16) | ((j ^ row) & 15);
-          x[h] = *reinterpret_cast<const u32x4*>(xs + row * kRowBytes + slot * 16);
-        }
-#pragma unroll
-        for (int b = 0; b < kNbw; ++b) {
-          u32x4 w;
-          if constexpr (GIVEN) {
-            const int i = (grp * kNbw + b) * 16 + m;
-            w = load_row8(A + (int64_t)(i < a.r ? i : a.r - 1) * a.lda, ch * kChunk + 8 * j, a.k);
-          } else {
-            w = signs_to_bf16x8((uint32_t)(sw[b] >> (8 * s)) & 0xFFu, smk);
-          }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) acc[b][h] = mfma16(w, x[h], acc[b][h]);
+          for (int w = 1; w < W; ++w) sum += red[(w * kTileRows + t) * kRedRow + i0 + e];
+          // ranks past r meet no U
+          p[e] = 32 * b + i0 + e < a.r ? sum : 0.0f;
         }
       }
     }
-    if constexpr (kKsub > 1) {
-      // the waves of a block meet in LDS, in order
-      __syncthreads();
-#pragma unroll
-      for (int b = 0; b < kNbw; ++b)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) red[((wave * kNbw + b) * 2 + h) * 64 + lane] = acc[b][h];
-      __syncthreads();
-      if (ksub == 0) {
-#pragma unroll
-        for (int b = 0; b < kNbw; ++b)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int q = 1; q < kKsub; ++q)
-              acc[b][h] += red[(((wave + q) * kNbw + b) * 2 + h) * 64 + lane];
-      }
+    __syncthreads();         // before the next copies
+  };
+
+  int id;
+  uint64_t rows;
+  if constexpr (GIVEN) {
+    // (a basis may hold an infinity, whose product with a zero column is NaN:
+    // one policy at a time)
+    for (int u = 0; pol.next(&id, &rows); ++u) {
+      if (u % n_deal != deal) continue;
+      clear();
+      pass(id, ~0u, -1, 0u, pol, 0);
+      finish(rows);
     }
-    if (ksub == 0) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int row = 16 * h + m;
-        if ((rows >> row) & 1) {
-          float* p = P + ((int64_t)split * a.T + t0 + row) * RP;
-#pragma unroll
-          for (int b = 0; b < kNbw; ++b) {
-            const int i = (grp * kNbw + b) * 16 + 4 * g;
-            f32x4 v = acc[b][h];
-            // columns past r meet no U
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = i + e < a.r ? v[e] : 0.0f;
-            *reinterpret_cast<f32x4*>(p + i) = v;
-          }
-        }
+  } else {
+    // Signs are finite, so the policies of a tile share its accumulators: each
+    // meets the tile with the other rows zeroed.
+    int ids[2] = {-1, -1};
+    uint32_t keep[2] = {0, 0};
+    uint64_t mine = 0;
+    int n = 0, u = 0, u_more = 0;
+    Policies rest = pol;
+    for (; pol.next(&id, &rows); ++u) {
+      if (u % n_deal != deal) continue;
+      mine |= rows;
+      if (n < 2) {
+        ids[n] = id;
+        keep[n] = ((rows >> m) & 1) ? ~0u : 0u;
+        rest = pol;
+        u_more = u + 1;
       }
+      ++n;
     }
+    if (n == 0) return;
+    clear();
+    // (alone in its tile: the other rows are not written)
+    pass(ids[0], n == 1 ? ~0u : keep[0], ids[1], keep[1], rest, u_more);
+    finish(mine);
   }
 }
 
@@ -269,177 +347,605 @@ __device__ __forceinline__ void load_u(const uint16_t* row, int K, int r, u32x4&
   lo = u32x4{0, 0, 0, 0};
 }
 
-// 8 columns of one row of out = Y + delta (or the bits of Y, COPY).
-template <bool COPY>
-__device__ __forceinline__ void write8(const uint16_t* y, uint16_t* o, int col, int d,
-                                       const float* delta) {
-  if (col + 8 <= d) {
-    u32x4 v = *reinterpret_cast<const u32x4*>(y + col);
-    if constexpr (!COPY) {
+// The pieces of the kernels below: a wave has 16 rows x 64 columns at a time.
+
+// P of row t at K .. K + 7 (its pieces of k added in order), scaled, as a pair.
+// RP == 16 fills only the first two lane groups.
+template <int RP>
+__device__ __forceinline__ const float* p_at(const float* P, int64_t t, int K) {
+  return P + t * RP + (RP >= 32 || K < RP ? K : 0);
+}
+template <int RP>
+__device__ __forceinline__ void p_pair(f32x4 v0, f32x4 v1, const float* src, int64_t piece,
+                                       int n_split, float sc, int K, u32x4& hi, u32x4& lo) {
+  for (int i = 1; i < n_split; ++i) {
+    src += piece;
+    v0 += *reinterpret_cast<const f32x4*>(src);
+    v1 += *reinterpret_cast<const f32x4*>(src + 4);
+  }
+  float x[8];
 #pragma unroll
-      for (int p = 0; p < 4; ++p)
-        v[p] = pack_bf16x2(bf16_lo(v[p]) + delta[2 * p], bf16_hi(v[p]) + delta[2 * p + 1]);
-    }
-    *reinterpret_cast<u32x4*>(o + col) = v;
+  for (int e = 0; e < 8; ++e) {
+    x[e] = (e < 4 ? v0[e & 3] : v1[e & 3]) * sc;
+    if (RP < 32) x[e] = K < RP ? x[e] : 0.0f;
+  }
+  split8(x, hi, lo);
+}
+
+// Orders a wave's LDS writes before its reads of what other lanes wrote.
+__device__ __forceinline__ void wave_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Results cross a per-wave stage in LDS, so that Y is read and out written in
+// whole 128-byte lines: 8 lanes a row, lane l columns 8 (l % 8) .. of rows l / 8
+// and l / 8 + 8.
+constexpr int kStageRow = 64 + 4;
+__device__ __forceinline__ void stage_sums(float* stage, const f32x4* sum) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int w = 0; w < 4; ++w)
+    *reinterpret_cast<f32x4*>(stage + (lane & 15) * kStageRow + 16 * w + 4 * (lane >> 4)) = sum[w];
+  wave_sync();
+}
+// (a group that ends past d is an aligned 16 bytes that hold an element of the
+// row; lanes past d re-read the row's first group and store nothing)
+__device__ __forceinline__ u32x4 load_y(const AdapterArgs& a, int64_t row, int col) {
+  const uint16_t* y = a.Y + (row < a.T ? row : a.T - 1) * a.ldy;
+  return __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(y + (col < a.d ? col : 0)));
+}
+__device__ __forceinline__ void store_out(const AdapterArgs& a, int64_t row, int col, u32x4 v) {
+  uint16_t* o = a.out + row * a.ldo;
+  if (col + 8 <= a.d) {
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(o + col));
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
-      if (col + e < d) {
-        if constexpr (COPY)
-          o[col + e] = y[col + e];
-        else
-          o[col + e] = f32_to_bf16(bf16_to_f32(y[col + e]) + delta[e]);
-      }
+      if (col + e < a.d) o[col + e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
   }
 }
+__device__ __forceinline__ u32x4 add_staged(u32x4 v, const float* stage, int r) {
+  const int lane = threadIdx.x & 63;
+  const f32x4 x = *reinterpret_cast<const f32x4*>(stage + r * kStageRow + 8 * (lane & 7));
+  const f32x4 y = *reinterpret_cast<const f32x4*>(stage + r * kStageRow + 8 * (lane & 7) + 4);
+  v[0] = pack_bf16x2(bf16_lo(v[0]) + x[0], bf16_hi(v[0]) + x[1]);
+  v[1] = pack_bf16x2(bf16_lo(v[1]) + x[2], bf16_hi(v[1]) + x[3]);
+  v[2] = pack_bf16x2(bf16_lo(v[2]) + y[0], bf16_hi(v[2]) + y[1]);
+  v[3] = pack_bf16x2(bf16_lo(v[3]) + y[2], bf16_hi(v[3]) + y[3]);
+  return v;
+}
 
-// NR blocks of 16 rows x 64 columns per wave, NW waves side by side along d.
-// RP: row length of P; NKS steps of 32 along the rank.
-template <int RP, class UT, bool VEC, int NR, int NW>
-__global__ __launch_bounds__(64 * NW) void adapter_expand_kernel(AdapterArgs a, int n_split,
-                                                                 float c, const float* __restrict__ P) {
+// One block, its policies one after the other with U read from memory: P, Y and
+// the policies are loaded once, the product is run for every policy and each row
+// keeps its own, so that only U's latency is paid per policy.  WHOLE, up
+// to rank 64 and with rows of U on 16-byte boundaries: all of U's operands are
+// loaded together; else a step of 32 along the rank at a time.
+template <int RP, class UT, bool VEC, bool WHOLE>
+__device__ __forceinline__ void direct_block(const AdapterArgs& a, int n_split, float c,
+                                             const float* __restrict__ P, int64_t row0, int col0,
+                                             float* stage) {
   constexpr int NKS = RP < 32 ? 1 : RP / 32;
-  constexpr bool kPair = sizeof(UT) == 4;   // U as hi + lo
+  constexpr bool kPair = sizeof(UT) == 4;
+  constexpr bool kWhole = WHOLE && NKS <= 2 && VEC;
+  constexpr int kHeld = kWhole ? NKS : 1;
+  const int lane = threadIdx.x & 63;
+  const int m = lane & 15;
+  const int g = lane >> 4;
+  const int lcol = col0 + 8 * (lane & 7);
+  const int64_t row = row0 + m;
+  const int64_t t = row < a.T ? row : a.T - 1;
+  u32x4 y[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) y[i] = load_y(a, row0 + (lane >> 3) + 8 * i, lcol);
+  f32x4 p[kHeld][2];
+  auto load_p = [&](int s, f32x4* q) LOGRA_INLINE {
+    const float* src = p_at<RP>(P, t, 32 * s + 8 * g);
+    q[0] = *reinterpret_cast<const f32x4*>(src);
+    q[1] = *reinterpret_cast<const f32x4*>(src + 4);
+  };
+  if constexpr (kWhole) {
+#pragma unroll
+    for (int s = 0; s < NKS; ++s) load_p(s, p[s]);
+  }
+  int id_m = row < a.T ? a.adapter[row] : -1;
+  if (id_m < 0 || (int64_t)id_m >= a.n) id_m = -1;
+  const float sc = id_m >= 0 ? c * a.scale[id_m] : 0.0f;
+  u32x4 ph[kHeld], pl[kHeld];
+  auto pair_p = [&](int s, const f32x4* q, u32x4& hi, u32x4& lo) LOGRA_INLINE {
+    const int K = 32 * s + 8 * g;
+    p_pair<RP>(q[0], q[1], p_at<RP>(P, t, K), a.T * RP, n_split, sc, K, hi, lo);
+  };
+  if constexpr (kWhole) {
+#pragma unroll
+    for (int s = 0; s < NKS; ++s) pair_p(s, p[s], ph[s], pl[s]);
+  }
+  f32x4 sum[4];
+#pragma unroll
+  for (int w = 0; w < 4; ++w) sum[w] = f32x4{0.f, 0.f, 0.f, 0.f};
+  uint64_t left = __ballot(id_m >= 0);
+  while (left) {
+    const int id = __builtin_amdgcn_readlane(id_m, __ffsll((unsigned long long)left) - 1);
+    const bool mine = id_m == id;
+    left &= ~__ballot(mine);
+    const UT* U = static_cast<const UT*>(a.U) + (int64_t)id * a.d * a.r;
+    f32x4 v[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) v[w] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto u_row = [&](int w) LOGRA_INLINE {
+      const int col = col0 + 16 * w + m;
+      return U + (int64_t)(col < a.d ? col : a.d - 1) * a.r;
+    };
+    auto product = [&](int w, const u32x4& uh, const u32x4& ul, const u32x4& hi, const u32x4& lo)
+                       LOGRA_INLINE {
+      v[w] = mfma16(uh, lo, v[w]);
+      if constexpr (kPair) v[w] = mfma16(ul, hi, v[w]);
+      v[w] = mfma16(uh, hi, v[w]);
+    };
+    if constexpr (kWhole) {
+      u32x4 uh[NKS][4], ul[NKS][4];
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int s = 0; s < NKS; ++s)
+          load_u<VEC>(u_row(w), 32 * s + 8 * g, a.r, uh[s][w], ul[s][w]);
+#pragma unroll
+      for (int w = 0; w < 4; ++w)
+#pragma unroll
+        for (int s = 0; s < NKS; ++s) product(w, uh[s][w], ul[s][w], ph[s], pl[s]);
+    } else {
+#pragma unroll 1
+      for (int s = 0; s < NKS; ++s) {
+        load_p(s, p[0]);
+        pair_p(s, p[0], ph[0], pl[0]);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          u32x4 uh, ul;
+          load_u<VEC>(u_row(w), 32 * s + 8 * g, a.r, uh, ul);
+          product(w, uh, ul, ph[0], pl[0]);
+        }
+      }
+    }
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[w][e] = mine ? v[w][e] : sum[w][e];
+  }
+  stage_sums(stage, sum);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int r = (lane >> 3) + 8 * i;
+    const int id = __shfl(id_m, r);
+    // (a row without a policy keeps its bits)
+    const u32x4 v = id >= 0 ? add_staged(y[i], stage, r) : y[i];
+    if (row0 + r < a.T) store_out(a, row0 + r, lcol, v);
+  }
+  wave_sync();
+}
+
+// Few rows: one wave, one block.
+template <int RP, class UT, bool VEC>
+__global__ __launch_bounds__(64) void adapter_block_kernel(AdapterArgs a, int n_split, float c,
+                                                           const float* __restrict__ P) {
+  __shared__ __attribute__((aligned(16))) float stage[16 * kStageRow];
+  const int n_cb = (a.d + 63) / 64;
+  direct_block<RP, UT, VEC, true>(a, n_split, c, P, (int64_t)(blockIdx.x / n_cb) * 16,
+                                  (int)(blockIdx.x % n_cb) * 64, stage);
+}
+
+// Many rows, rank up to 64 and rows of U on 16-byte boundaries: four waves side by
+// side along d walk down up to kRowBlocks blocks.  U's operands of the policy at
+// hand stay in registers (64 at rank 64 in fp32) and are read again only where the
+// policy changes; P is loaded one block ahead and Y three.  All work-groups of a
+// large call are resident at once (two to a CU): with half the rows in each, the
+// second half paid the first loads' latencies again.
+constexpr int kRowBlocks = 16;
+
+template <int RP, class UT>
+__global__ __launch_bounds__(256, 2) void adapter_rows_kernel(AdapterArgs a, int n_split, float c,
+                                                              int n_blocks,
+                                                              const float* __restrict__ P) {
+  constexpr int NKS = RP < 32 ? 1 : RP / 32;
+  constexpr bool kPair = sizeof(UT) == 4;
+  constexpr int kSets = kRowBlocks / 4;
+  __shared__ __attribute__((aligned(16))) float stage_all[4][16 * kStageRow];
   const int lane = threadIdx.x & 63;
   const int wave = threadIdx.x >> 6;
   const int m = lane & 15;
   const int g = lane >> 4;
-  const int n_cb = (a.d + 64 * NW - 1) / (64 * NW);
-  const int64_t rb0 = (int64_t)(blockIdx.x / n_cb) * (16 * NR);
-  const int col0 = ((int)(blockIdx.x % n_cb) * NW + wave) * 64;
+  float* const stage = stage_all[wave];
+  const int n_cb = (a.d + 255) / 256;
+  const int group = (int)(blockIdx.x / n_cb);
+  const int col0 = (xcd_spread((int)(blockIdx.x % n_cb), group, n_cb) * 4 + wave) * 64;
   if (col0 >= a.d) return;
-  const int64_t myrow = rb0 + lane;
-  Policies pol(a.adapter, myrow, lane < 16 * NR && myrow < a.T, a.n);
+  const int64_t rb0 = (int64_t)group * (16 * n_blocks);
+  const int lcol = col0 + 8 * (lane & 7);
+  const int64_t rest = (a.T - rb0 + 15) / 16;
+  const int nb = rest < n_blocks ? (int)rest : n_blocks;
 
-  // rows without a policy
-  if (a.out != a.Y) {
-    const uint64_t none = __ballot(lane < 16 * NR && myrow < a.T) & ~pol.left;
-    if (none) {
+  // Policies and factors of the rows, 64 to a register: a factor's address waits
+  // for its policy, and so for every load issued before.
+  int ids[kSets];
+  float scs[kSets];
 #pragma unroll
-      for (int b = 0; b < NR; ++b) {
-        const int64_t t = rb0 + 16 * b + m;
-        if ((none >> (16 * b + m)) & 1) {
-          write8<true>(a.Y + t * a.ldy, a.out + t * a.ldo, col0 + 16 * g, a.d, nullptr);
-          write8<true>(a.Y + t * a.ldy, a.out + t * a.ldo, col0 + 16 * g + 8, a.d, nullptr);
+  for (int i = 0; i < kSets; ++i) {
+    const int64_t row = rb0 + 64 * i + lane;
+    const int id = 64 * i + lane < 16 * n_blocks && row < a.T ? a.adapter[row] : -1;
+    ids[i] = id < 0 || (int64_t)id >= a.n ? -1 : id;
+  }
+#pragma unroll
+  for (int i = 0; i < kSets; ++i) scs[i] = ids[i] >= 0 ? a.scale[ids[i]] : 0.0f;
+
+  // Nothing may use a prefetched value before its block, or the wait comes with
+  // the load.
+  f32x4 p[2][NKS][2];
+  u32x4 y[4][2];
+  auto load_p = [&](int b, f32x4 (*q)[2]) LOGRA_INLINE {
+    const int64_t row = rb0 + 16 * b + m;
+#pragma unroll
+    for (int s = 0; s < NKS; ++s) {
+      const float* src = p_at<RP>(P, row < a.T ? row : a.T - 1, 32 * s + 8 * g);
+      q[s][0] = *reinterpret_cast<const f32x4*>(src);
+      q[s][1] = *reinterpret_cast<const f32x4*>(src + 4);
+    }
+  };
+  auto load_rows = [&](int b, u32x4* v) LOGRA_INLINE {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) v[i] = load_y(a, rb0 + 16 * b + (lane >> 3) + 8 * i, lcol);
+  };
+  int cur = -1;
+  u32x4 uh[NKS][4], ul[NKS][4];
+  auto load_policy = [&](int id) LOGRA_INLINE {
+    cur = id;
+    const UT* U = static_cast<const UT*>(a.U) + (int64_t)id * a.d * a.r;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      const int col = col0 + 16 * w + m;
+      const UT* urow = U + (int64_t)(col < a.d ? col : a.d - 1) * a.r;
+#pragma unroll
+      for (int s = 0; s < NKS; ++s) load_u<true>(urow, 32 * s + 8 * g, a.r, uh[s][w], ul[s][w]);
+    }
+  };
+  auto compute = [&](int b, const f32x4 (*q)[2], const u32x4* yv) LOGRA_INLINE {
+    int id_m = ids[0];
+    float sc = scs[0];
+#pragma unroll
+    for (int i = 1; i < kSets; ++i) {
+      id_m = b >= 4 * i ? ids[i] : id_m;
+      sc = b >= 4 * i ? scs[i] : sc;
+    }
+    id_m = __shfl(id_m, 16 * (b & 3) + m);
+    sc = c * __shfl(sc, 16 * (b & 3) + m);
+    const int64_t row = rb0 + 16 * b + m;
+    u32x4 ph[NKS], pl[NKS];
+#pragma unroll
+    for (int s = 0; s < NKS; ++s) {
+      const int K = 32 * s + 8 * g;
+      p_pair<RP>(q[s][0], q[s][1], p_at<RP>(P, row < a.T ? row : a.T - 1, K), a.T * RP, n_split, sc,
+                 K, ph[s], pl[s]);
+    }
+    f32x4 sum[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) sum[w] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto product = [&](int w, f32x4 v) LOGRA_INLINE {
+#pragma unroll
+      for (int s = 0; s < NKS; ++s) {
+        v = mfma16(uh[s][w], pl[s], v);
+        if constexpr (kPair) v = mfma16(ul[s][w], ph[s], v);
+        v = mfma16(uh[s][w], ph[s], v);
+      }
+      return v;
+    };
+    uint64_t left = __ballot(id_m >= 0);
+    if (left != 0) {
+      int id = __builtin_amdgcn_readlane(id_m, __ffsll((unsigned long long)left) - 1);
+      left &= ~__ballot(id_m == id);
+      if (id != cur) load_policy(id);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) sum[w] = product(w, sum[w]);
+      // (rows of no policy take what they get here and drop it below)
+      while (left != 0) {
+        id = __builtin_amdgcn_readlane(id_m, __ffsll((unsigned long long)left) - 1);
+        const bool mine = id_m == id;
+        left &= ~__ballot(mine);
+        load_policy(id);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const f32x4 v = product(w, f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sum[w][e] = mine ? v[e] : sum[w][e];
         }
+      }
+    }
+    stage_sums(stage, sum);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = (lane >> 3) + 8 * i;
+      const int64_t orow = rb0 + 16 * b + r;
+      const int id = __shfl(id_m, r);
+      // (a row without a policy keeps its bits)
+      const u32x4 added = add_staged(yv[i], stage, r);
+      u32x4 v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = id >= 0 ? added[e] : yv[i][e];
+      if (orow < a.T) store_out(a, orow, lcol, v);
+    }
+    wave_sync();
+  };
+  // Loads complete in the order of their issue, so a block's P goes before the Y
+  // issued with it.
+  load_p(0, p[0]);
+#pragma unroll
+  for (int j = 0; j < 3; ++j)
+    if (j < nb) load_rows(j, y[j]);
+  for (int b0 = 0; b0 < nb; b0 += 4) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int b = b0 + j;
+      if (b >= nb) break;
+      if (b + 1 < nb) load_p(b + 1, p[(j + 1) & 1]);
+      if (b + 3 < nb) load_rows(b + 3, y[(j + 3) & 3]);
+      compute(b, p[j & 1], y[j]);
+    }
+  }
+}
+
+// Many rows otherwise: eight waves share a strip of 64 columns and take every
+// eighth of its blocks, up to kStripBlocks each.  U's operands of one policy at a
+// time lie in LDS in operand order (converted once for the work-group's rows, 64
+// KB at r = 256 in fp32).  Blocks whose rows belong to several policies (or to
+// none, where they have to be copied) go through direct_block instead, once.
+constexpr int kStripBlocks = 8;
+constexpr int kStripWaves = 8;
+
+template <int RP, class UT, bool VEC>
+__global__ __launch_bounds__(64 * kStripWaves, 2) void adapter_strip_kernel(AdapterArgs a, int n_split, float c,
+                                                            int n_blocks,
+                                                            const float* __restrict__ P) {
+  constexpr int NKS = RP < 32 ? 1 : RP / 32;
+  constexpr bool kPair = sizeof(UT) == 4;
+  constexpr int kParts = kPair ? 2 : 1;
+  constexpr bool kAhead = RP <= 128;    // P of a larger rank is not held ahead
+  constexpr int kSets = kStripBlocks / 4;
+  __shared__ u32x4 us[NKS * 4 * kParts * 64];
+  __shared__ __attribute__((aligned(16))) float stage_all[kStripWaves][16 * kStageRow];
+  __shared__ int candidate[kStripWaves];
+  const int lane = threadIdx.x & 63;
+  const int wave = threadIdx.x >> 6;
+  const int m = lane & 15;
+  const int g = lane >> 4;
+  float* const stage = stage_all[wave];
+  const int n_cb = (a.d + 63) / 64;
+  const int group = (int)(blockIdx.x / n_cb);
+  const int col0 = xcd_spread((int)(blockIdx.x % n_cb), group, n_cb) * 64;
+  // block b of this wave starts at row rb0 + kBlockRows b
+  constexpr int kBlockRows = 16 * kStripWaves;
+  const int64_t rb0 = (int64_t)group * (kBlockRows * n_blocks) + 16 * wave;
+  const int lcol = col0 + 8 * (lane & 7);
+
+  // policies and factors of the wave's rows, 64 to a register; `left`: rows of
+  // the blocks with one policy, `apart`: the other blocks to do (bit b)
+  int ids[kSets];
+  float scs[kSets];
+  uint64_t left[kSets];
+  uint32_t apart = 0;
+#pragma unroll
+  for (int i = 0; i < kSets; ++i) {
+    const int b = 4 * i + (lane >> 4);
+    const int64_t row = rb0 + (int64_t)kBlockRows * b + m;
+    const bool in = b < n_blocks && row < a.T;
+    const int id = in ? a.adapter[row] : -1;
+    ids[i] = id < 0 || (int64_t)id >= a.n ? -1 : id;
+    const uint64_t rows = __ballot(in);
+    const uint64_t odd = __ballot(in && ids[i] != __shfl(ids[i], lane & 48));
+    left[i] = __ballot(ids[i] >= 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint64_t block = uint64_t(0xFFFF) << (16 * j);
+      // (rows that go in place need no copy)
+      const bool alike = (odd & block) == 0 && ((left[i] & block) != 0 || a.out == a.Y);
+      if ((rows & block) != 0 && !alike) {
+        apart |= 1u << (4 * i + j);
+        left[i] &= ~block;
       }
     }
   }
+#pragma unroll
+  for (int i = 0; i < kSets; ++i) scs[i] = ids[i] >= 0 ? c * a.scale[ids[i]] : 0.0f;
+  auto of_set = [&](const int b, const auto* v) {
+    auto x = v[0];
+#pragma unroll
+    for (int i = 1; i < kSets; ++i) x = b >= 4 * i ? v[i] : x;
+    return x;
+  };
+  // blocks (bit b) with a row in the given sets
+  auto blocks_of = [&](const uint64_t* rows) {
+    uint32_t need = 0;
+#pragma unroll
+    for (int b = 0; b < kStripBlocks; ++b)
+      need |= ((rows[b / 4] >> (16 * (b & 3))) & 0xFFFFu) ? 1u << b : 0u;
+    return need;
+  };
+  for (; apart; apart &= apart - 1)
+    direct_block<RP, UT, VEC, false>(a, n_split, c, P, rb0 + kBlockRows * __builtin_ctz(apart), col0,
+                                     stage);
 
-  int id;
-  uint64_t rows;
-  while (pol.next(&id, &rows)) {
+  for (;;) {
+    // the work-group's next policy: the first one left in its first wave with any
+    int next = -1;
+#pragma unroll
+    for (int i = kSets - 1; i >= 0; --i)
+      if (left[i])
+        next = __builtin_amdgcn_readlane(ids[i], __ffsll((unsigned long long)left[i]) - 1);
+    if (lane == 0) candidate[wave] = next;
+    __syncthreads();       // (and every wave is done with us)
+    int id = -1;
+#pragma unroll
+    for (int w = kStripWaves - 1; w >= 0; --w) id = candidate[w] >= 0 ? candidate[w] : id;
+    if (id < 0) break;
     const UT* U = static_cast<const UT*>(a.U) + (int64_t)id * a.d * a.r;
-    const float sc = c * a.scale[id];
-    f32x4 acc[NR][4];
+    for (int f = wave; f < 4 * NKS; f += kStripWaves) {   // an operand (s, w) a wave
+      const int s = f >> 2;
+      const int col = col0 + 16 * (f & 3) + m;
+      u32x4 hi, lo;
+      load_u<VEC>(U + (int64_t)(col < a.d ? col : a.d - 1) * a.r, 32 * s + 8 * g, a.r, hi, lo);
+      us[f * kParts * 64 + lane] = hi;
+      if constexpr (kPair) us[(f * kParts + 1) * 64 + lane] = lo;
+    }
+    __syncthreads();
+
+    uint64_t mine[kSets];
 #pragma unroll
-    for (int b = 0; b < NR; ++b)
+    for (int i = 0; i < kSets; ++i) {
+      mine[i] = __ballot(ids[i] == id) & left[i];
+      left[i] &= ~mine[i];
+    }
+    uint32_t need = blocks_of(mine);
+    const int nb = __builtin_popcount(need);
+    uint32_t order = 0;    // four bits for each block to do
+    for (int j = 0; need; ++j, need &= need - 1) order |= (uint32_t)__builtin_ctz(need) << (4 * j);
+
+    f32x4 p[2][kAhead ? NKS : 1][2];
+    u32x4 y[4][2];
+    auto load_p = [&](int b, f32x4 (*q)[2]) LOGRA_INLINE {
+      if constexpr (kAhead) {
+        const int64_t row = rb0 + kBlockRows * b + m;
 #pragma unroll
-      for (int t = 0; t < 4; ++t) acc[b][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 1
-    for (int s = 0; s < NKS; ++s) {
-      const int K = 32 * s + 8 * g;
-      u32x4 uh[4], ul[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const int col = col0 + (m >> 2) * 16 + 4 * t + (m & 3);
-        load_u<VEC>(U + (int64_t)(col < a.d ? col : a.d - 1) * a.r, K, a.r, uh[t], ul[t]);
-      }
-#pragma unroll
-      for (int b = 0; b < NR; ++b) {
-        if (((rows >> (16 * b)) & 0xFFFFu) == 0) continue;
-        // rows of other policies give columns that are not used
-        const int64_t row = rb0 + 16 * b + m;
-        const int64_t t = row < a.T ? row : a.T - 1;
-        float p[8] = {};
-        if (RP >= 32 || K < RP) {
-          for (int q = 0; q < n_split; ++q) {
-            const float* src = P + ((int64_t)q * a.T + t) * RP + K;
-            const f32x4 lo4 = *reinterpret_cast<const f32x4*>(src);
-            const f32x4 hi4 = *reinterpret_cast<const f32x4*>(src + 4);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              p[e] += lo4[e];
-              p[4 + e] += hi4[e];
-            }
-          }
+        for (int s = 0; s < NKS; ++s) {
+          const float* src = p_at<RP>(P, row < a.T ? row : a.T - 1, 32 * s + 8 * g);
+          q[s][0] = *reinterpret_cast<const f32x4*>(src);
+          q[s][1] = *reinterpret_cast<const f32x4*>(src + 4);
         }
+      }
+    };
+    auto load_rows = [&](int b, u32x4* v) LOGRA_INLINE {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) p[e] *= sc;
+      for (int i = 0; i < 2; ++i) v[i] = load_y(a, rb0 + kBlockRows * b + (lane >> 3) + 8 * i, lcol);
+    };
+    auto compute = [&](int b, const f32x4 (*q)[2], const u32x4* yv) LOGRA_INLINE {
+      const float sc = __shfl(of_set(b, scs), 16 * (b & 3) + m);
+      const int64_t row = rb0 + kBlockRows * b + m;
+      f32x4 sum[4];
+#pragma unroll
+      for (int w = 0; w < 4; ++w) sum[w] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int s = 0; s < NKS; ++s) {
+        const int K = 32 * s + 8 * g;
+        const float* src = p_at<RP>(P, row < a.T ? row : a.T - 1, K);
+        f32x4 v0, v1;
+        if constexpr (kAhead) {
+          v0 = q[s][0];
+          v1 = q[s][1];
+        } else {
+          v0 = *reinterpret_cast<const f32x4*>(src);
+          v1 = *reinterpret_cast<const f32x4*>(src + 4);
+        }
         u32x4 ph, pl;
-        split8(p, ph, pl);
+        p_pair<RP>(v0, v1, src, a.T * RP, n_split, sc, K, ph, pl);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          acc[b][w] = mfma16(uh[w], pl, acc[b][w]);
-          if constexpr (kPair) acc[b][w] = mfma16(ul[w], ph, acc[b][w]);
-          acc[b][w] = mfma16(uh[w], ph, acc[b][w]);
+          const u32x4 uh = us[((s * 4 + w) * kParts) * 64 + lane];
+          sum[w] = mfma16(uh, pl, sum[w]);
+          if constexpr (kPair)
+            sum[w] = mfma16(us[((s * 4 + w) * kParts + 1) * 64 + lane], ph, sum[w]);
+          sum[w] = mfma16(uh, ph, sum[w]);
         }
       }
-    }
+      stage_sums(stage, sum);
+      const uint32_t rows = (uint32_t)(of_set(b, mine) >> (16 * (b & 3)));
 #pragma unroll
-    for (int b = 0; b < NR; ++b) {
-      if ((rows >> (16 * b + m)) & 1) {
-        const int64_t t = rb0 + 16 * b + m;
-        float delta[16];
+      for (int i = 0; i < 2; ++i) {
+        const int r = (lane >> 3) + 8 * i;
+        const u32x4 v = add_staged(yv[i], stage, r);
+        if ((rows >> r) & 1) store_out(a, rb0 + kBlockRows * b + r, lcol, v);
+      }
+      wave_sync();
+    };
+    // Loads complete in the order of their issue, so a block's P goes before the
+    // Y issued with it.
+    auto block = [&](int j) { return (int)((order >> (4 * j)) & 15u); };
+    if (nb > 0) load_p(block(0), p[0]);
 #pragma unroll
-        for (int w = 0; w < 4; ++w)
+    for (int j = 0; j < 3; ++j)
+      if (j < nb) load_rows(block(j), y[j]);
+    for (int j0 = 0; j0 < nb; j0 += 4) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) delta[4 * w + e] = acc[b][w][e];
-        write8<false>(a.Y + t * a.ldy, a.out + t * a.ldo, col0 + 16 * g, a.d, delta);
-        write8<false>(a.Y + t * a.ldy, a.out + t * a.ldo, col0 + 16 * g + 8, a.d, delta + 8);
+      for (int i = 0; i < 4; ++i) {
+        const int j = j0 + i;
+        if (j >= nb) break;
+        if (j + 1 < nb) load_p(block(j + 1), p[(i + 1) & 1]);
+        if (j + 3 < nb) load_rows(block(j + 3), y[(i + 3) & 3]);
+        compute(block(j), p[i & 1], y[i]);
       }
     }
   }
 }
 
 // ---------------------------------------------------------------- launches
-constexpr int64_t kFill = 512;   // work-groups that keep the chip busy
+constexpr int64_t kCus = 256;
 
-template <int NB>
+template <int RP>
 void launch_project(const AdapterArgs& a, const AdapterPlan& p, float* P, hipStream_t s) {
+  constexpr int NB = RP < 32 ? 1 : RP / 32;
   const int64_t tiles = (a.T + kTileRows - 1) / kTileRows;
   const int64_t base = tiles * p.n_split;
-  int64_t deal = (kFill + base - 1) / base;
+  int64_t deal = kCus / base;
+  if (deal < 1) deal = 1;
   if (deal > kTileRows) deal = kTileRows;
   if (deal > a.n) deal = a.n;
-  const dim3 grid((unsigned)(base * deal));
+  const dim3 grid((unsigned)(base * deal)), block(64 * proj_waves(NB));
   if (a.A)
-    hipLaunchKernelGGL((adapter_project_kernel<NB, true>), grid, dim3(kThreads), 0, s, a, p.n_split,
+    hipLaunchKernelGGL((adapter_project_kernel<NB, true>), grid, block, 0, s, a, RP, p.n_split,
                        p.chunks_per_split, (int)deal, P);
   else
-    hipLaunchKernelGGL((adapter_project_kernel<NB, false>), grid, dim3(kThreads), 0, s, a,
-                       p.n_split, p.chunks_per_split, (int)deal, P);
+    hipLaunchKernelGGL((adapter_project_kernel<NB, false>), grid, block, 0, s, a, RP, p.n_split,
+                       p.chunks_per_split, (int)deal, P);
 }
 
 template <int RP, class UT, bool VEC>
-void launch_expand_vec(const AdapterArgs& a, const AdapterPlan& p, float c, const float* P,
-                       hipStream_t s) {
-  const int64_t big = ((a.T + 63) / 64) * ((a.d + 255) / 256);
-  if (big >= kFill / 2) {
-    hipLaunchKernelGGL((adapter_expand_kernel<RP, UT, VEC, 4, 4>), dim3((unsigned)big), dim3(256), 0,
-                       s, a, p.n_split, c, P);
-  } else {
-    const int64_t small = ((a.T + 15) / 16) * ((a.d + 63) / 64);
-    hipLaunchKernelGGL((adapter_expand_kernel<RP, UT, VEC, 1, 1>), dim3((unsigned)small), dim3(64),
-                       0, s, a, p.n_split, c, P);
+void launch_expand(const AdapterArgs& a, const AdapterPlan& p, float c, const float* P,
+                   hipStream_t s) {
+  const int64_t n_cb = (a.d + 63) / 64;
+  const int64_t blocks = (a.T + 15) / 16;
+  // eight blocks to a SIMD and more: walk down several with one U
+  if (blocks * n_cb >= 8 * 4 * kCus) {
+    if constexpr (RP <= 64 && VEC) {
+      const int64_t wide = (a.d + 255) / 256;
+      int64_t per = (blocks * wide + 2 * kCus - 1) / (2 * kCus);   // two work-groups to a CU
+      per = per < 1 ? 1 : per > kRowBlocks ? kRowBlocks : per;
+      hipLaunchKernelGGL((adapter_rows_kernel<RP, UT>),
+                         dim3((unsigned)((blocks + per - 1) / per * wide)), dim3(256), 0, s, a,
+                         p.n_split, c, (int)per, P);
+    } else {
+      int64_t per = blocks * n_cb / (kStripWaves * kCus);
+      per = per < 1 ? 1 : per > kStripBlocks ? kStripBlocks : per;
+      const int64_t rows = kStripWaves * per;
+      hipLaunchKernelGGL((adapter_strip_kernel<RP, UT, VEC>),
+                         dim3((unsigned)((blocks + rows - 1) / rows * n_cb)),
+                         dim3(64 * kStripWaves), 0, s, a, p.n_split, c, (int)per, P);
+    }
+    return;
   }
+  hipLaunchKernelGGL((adapter_block_kernel<RP, UT, VEC>), dim3((unsigned)(blocks * n_cb)), dim3(64),
+                     0, s, a, p.n_split, c, P);
 }
 
 template <int RP>
 void launch_both(const AdapterArgs& a, bool u_f32, const AdapterPlan& p, float c, float* P,
                  hipStream_t s) {
-  launch_project<RP / 16>(a, p, P, s);
+  launch_project<RP>(a, p, P, s);
   const bool vec = a.r % 8 == 0 && (reinterpret_cast<uintptr_t>(a.U) & 15) == 0;
   if (u_f32) {
     if (vec)
-      launch_expand_vec<RP, float, true>(a, p, c, P, s);
+      launch_expand<RP, float, true>(a, p, c, P, s);
     else
-      launch_expand_vec<RP, float, false>(a, p, c, P, s);
+      launch_expand<RP, float, false>(a, p, c, P, s);
   } else {
     if (vec)
-      launch_expand_vec<RP, uint16_t, true>(a, p, c, P, s);
+      launch_expand<RP, uint16_t, true>(a, p, c, P, s);
     else
-      launch_expand_vec<RP, uint16_t, false>(a, p, c, P, s);
+      launch_expand<RP, uint16_t, false>(a, p, c, P, s);
   }
 }
 
@@ -452,16 +958,19 @@ bool make_adapter_plan(int64_t T, int64_t d, int64_t k, int r, AdapterPlan* p) {
   p->rp = r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : r <= 128 ? 128 : 256;
   const int64_t tiles = (T + kTileRows - 1) / kTileRows;
   const int64_t chunks = (k + kChunk - 1) / kChunk;
-  int64_t split = (kFill + tiles - 1) / tiles;
-  if (split > chunks) split = chunks;
-  if (split > 16) split = 16;
+  // pieces of k while tiles leave CUs without one (a work-group has a CU's LDS
+  // to itself), each with a chunk for every wave
+  const int64_t waves = proj_waves(p->rp / 32);
+  int64_t split = (kCus + tiles - 1) / tiles;
+  if (split > (chunks + waves - 1) / waves) split = (chunks + waves - 1) / waves;
+  if (split > 8) split = 8;
   const int64_t per = (chunks + split - 1) / split;
   p->chunks_per_split = (int)per;
   p->n_split = (int)((chunks + per - 1) / per);
   p->total = (size_t)round_up((int64_t)p->n_split * T * p->rp * 4, 256);
   // (flat grids: work-groups, and threads below 2^32)
   const int64_t most = (int64_t(1) << 24) - 1;
-  return tiles * p->n_split <= most && ((T + 63) / 64) * ((d + 255) / 256) <= most;
+  return tiles * p->n_split <= most / 2 && (T + 63) / 64 * ((d + 63) / 64) / 16 <= most / 2;
 }
 
 hipError_t launch_adapter(const AdapterArgs& a, bool u_f32, const AdapterPlan& p, char* ws,

@@ -93,6 +93,10 @@ SHAPES = [
     (200, 1536, 1000, 16, 16, "mixed"), (129, 300, 515, 128, 3, "runs"), (70, 264, 136, 250, 2, "mixed"),
     (70, 264, 136, 256, 70, "mixed"), (1030, 512, 1028, 64, 4, "runs"), (2000, 264, 2056, 8, 3, "mixed"),
     (1500, 1000, 1031, 24, 6, "runs"),
+    # many rows and columns
+    (4100, 264, 1100, 64, 5, "runs"), (4099, 2500, 1096, 256, 3, "runs"),
+    (3000, 136, 1501, 100, 4, "mixed"), (3001, 300, 1500, 128, 9, "runs"),
+    (9000, 520, 260, 32, 40, "runs"), (2100, 5000, 1024, 16, 2, "one"),
 ]
 
 
