@@ -2,34 +2,40 @@
 // tokens under softmax(z / tau), the entropy of that distribution and its most
 // probable tokens, in one pass over the logits.
 //
-// Mathematics.  With m the largest logit of a row, d_j = (z_j - m) log2(e) / tau
+// Mathematics.  With a reference logit m of the row, d_j = (z_j - m) log2(e) / tau
 // and w_j = 2^d_j, a row needs s = sum w and u = sum w d:
-//   lse = m / tau + ln s,   logp = (z_target - m) / tau - ln s,
-//   H = ln s - ln(2) u / s  (both terms >= 0: no cancellation).
-// Each thread keeps (m, s, u) about its own running maximum (a rescale when a
-// group of its elements raises it), the states of a wave meet in a butterfly
-// and those of a row's waves in LDS, always in the same order.  m is
-// subtracted from the unscaled logit, which is exact for the tokens that carry
-// weight, so the exponent's rounding is relative to d and not to z / tau.
-// Masked tokens: z = -inf gives w = 0; d is clamped at kLow in u alone, so that
-// 0 * -inf does not arise while NaN (and +inf, which becomes NaN) still reach
-// s.  m starts at the lowest finite float instead of -inf: no case of its own
-// for a thread that has seen nothing yet.
-//
+//   lse = m / tau + ln s,   logp = ln(2) d_target - ln s,
+//   H = ln s - ln(2) u / s.
+// None of the three depends on m, which need only be near enough to the largest
+// logit that no weight overflows: a thread keeps the largest of the group that
+// set it and looks at its elements' maximum again only when a group's weights
+// sum to more than 2^10.  d is one fused step, z l2t - mc with l2t = log2(e) /
+// tau and mc = m l2t rounded: that rounding is the same for every token of the
+// row, cancels in logp and H, and is added back in lse, so rows far from zero
+// keep their accuracy.  Where m l2t is past fp32's range (a row at the type's
+// lowest value) mc is infinite, the fused step fails for every group, and the
+// careful path takes the difference first.  That path also takes the groups with
+// a masked token (z = -inf: w = 0, d clamped at kLow in u, so that 0 * -inf does
+// not arise); NaN, and +inf, which becomes NaN, still reach s.
+// The states of a wave meet in a butterfly and those of a row's waves in LDS,
+// always in the same order.
 // Alternatives.  Value and index of a token make one 64-bit key (the float's
-// bits in an order-preserving form above the inverted index), so "larger
-// logit, then lower index" is one integer comparison and keys are distinct:
-// the result does not depend on the order of anything.  A wave keeps its 64
-// best keys sorted over its lanes.  A group of elements is looked at closer
-// only when its largest value (already at hand for the softmax) beats the
-// n_top-th key's; passing elements are collected in LDS, and 64 of them at a
-// time are sorted by a bitonic network and merged in.  On a wave's first group
-// each lane first offers its own maximum: one sort then gives a threshold that
-// nearly all other elements fail.
+// bits in an order-preserving form above the inverted index), so "larger logit,
+// then lower index" is one integer comparison and keys are distinct: the result
+// does not depend on the order of anything.  What the stream keeps are not tokens
+// but runs of neighbours (a lane's 16 bytes), keyed by their largest logit: the
+// n_top best runs hold the n_top best tokens, because each run before a token's
+// own has a better one.  A run whose largest logit (one comparison) does not beat
+// the n_top-th so far is dropped; others wait in LDS, and 64 of them at a time are
+// sorted by a bitonic network and merged in.  On a wave's first group the lanes'
+// maxima alone are sorted (32-bit values): their n_top-th is a threshold that most
+// other runs fail, so that usually all of a work-group's keys fit one sort at the
+// end.  The best runs' tokens are then read again and sorted.
 //
-// Bound: the stream of the logits.  One work-group per row where the rows
-// fill the chip; fewer rows are cut into pieces whose states and keys a second
-// kernel joins.
+// Bound: the stream of the logits and, close behind it, the vector unit (eight
+// elements cost about 70 issue slots, 32 of them the exponentials).  One
+// work-group per row where the rows fill the chip; fewer rows are cut into pieces
+// whose states and keys a second kernel joins.
 #include <math.h>
 
 #include "common.hpp"
@@ -54,10 +60,22 @@ struct State {
   float m, s, u;
 };
 
+// d of logit z about the reference m: the fused step where m l2t is finite.
+__device__ __forceinline__ float exponent(float z, float m, float mc, float l2t) {
+  return isfinite(mc) ? fmaf(z, l2t, -mc) : (z - m) * l2t;
+}
+// The reference a as seen from the reference M >= a, clamped: a difference of the
+// rounded products that the weights were formed with (a fused one would not be).
+__device__ __forceinline__ float shift(float a, float M, float l2t) {
+#pragma clang fp contract(off)
+  const float ca = a * l2t, cM = M * l2t;
+  return fmaxf(isfinite(ca) && isfinite(cM) ? ca - cM : (a - M) * l2t, kLow);
+}
+
 __device__ __forceinline__ State merge_states(const State& a, const State& b, float l2t) {
   const float M = fmaxf(a.m, b.m);
-  const float da = fmaxf((a.m - M) * l2t, kLow);
-  const float db = fmaxf((b.m - M) * l2t, kLow);
+  const float da = shift(a.m, M, l2t);
+  const float db = shift(b.m, M, l2t);
   const float fa = exp2_normal(da), fb = exp2_normal(db);
   State o;
   o.m = M;
@@ -78,23 +96,42 @@ __device__ __forceinline__ State wave_state(State st, float l2t) {
   return st;
 }
 
-// Adds G elements whose maximum is gmax (-inf where there is none).
+// Adds G elements; mc = st.m l2t goes along.
 template <int G>
-__device__ __forceinline__ void add_group(State& st, const float* z, float gmax, float l2t) {
-  if (gmax > st.m) {
-    const float dm = fmaxf((st.m - gmax) * l2t, kLow);
-    const float f = exp2_normal(dm);
-    st.u = f * fmaf(st.s, dm, st.u);
-    st.s *= f;
-    st.m = gmax;
-  }
+__device__ __forceinline__ void add_group(State& st, float& mc, const float* z, float l2t) {
+  float gs = 0.0f, gu = 0.0f;
 #pragma unroll
   for (int e = 0; e < G; ++e) {
-    const float d = (z[e] - st.m) * l2t;
+    const float d = fmaf(z[e], l2t, -mc);
     const float w = exp2_normal(d);
-    st.s += w;
-    st.u = fmaf(w, fmaxf(d, kLow), st.u);
+    gs += w;
+    gu = fmaf(w, d, gu);
   }
+  // (2^10: the reference stays near enough for H to lose no more than ln 2^10
+  // roundings where ln s and u / s nearly cancel)
+  if (__builtin_expect(!(gs <= 0x1p10f) || gu != gu, 0)) {
+    float gmax = z[0];
+#pragma unroll
+    for (int e = 1; e < G; ++e) gmax = fmaxf(gmax, z[e]);
+    if (gmax > st.m) {
+      const float dm = shift(st.m, gmax, l2t);
+      const float f = exp2_normal(dm);
+      st.u = f * fmaf(st.s, dm, st.u);
+      st.s *= f;
+      st.m = gmax;
+      mc = gmax * l2t;
+    }
+    gs = gu = 0.0f;
+#pragma unroll
+    for (int e = 0; e < G; ++e) {
+      const float d = exponent(z[e], st.m, mc, l2t);
+      const float w = exp2_normal(d);
+      gs += w;
+      gu = fmaf(w, fmaxf(d, kLow), gu);
+    }
+  }
+  st.s += gs;
+  st.u += gu;
 }
 
 // ---------------------------------------------------------------- best keys
@@ -109,125 +146,237 @@ __device__ __forceinline__ float key_value(u64 key) {
 }
 __device__ __forceinline__ int key_index(u64 key) { return (int)(0xFFFFFFFFu - (uint32_t)key); }
 
-__device__ __forceinline__ u64 shfl_xor64(u64 x, int mask) {
-  const uint32_t lo = __shfl_xor((uint32_t)x, mask);
-  const uint32_t hi = __shfl_xor((uint32_t)(x >> 32), mask);
-  return ((u64)hi << 32) | lo;
+// The key of lane l ^ J, by moves inside the vector unit (a __shfl_xor goes
+// through LDS; the sorts below are chains of these): J = 1, 2 permute a quad;
+// reversing 8 lanes (l ^ 7) and then each quad (l ^ 3) is l ^ 4, reversing 16 and
+// then 8 is l ^ 8; 16 and 32 swap row pairs and wave halves.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t x) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, CTRL, 0xF, 0xF, true);
 }
-__device__ __forceinline__ u64 compare_exchange(u64 x, int j, bool keep_max) {
-  const u64 y = shfl_xor64(x, j);
+constexpr int kQuadXor1 = 0xB1, kQuadXor2 = 0x4E, kQuadXor3 = 0x1B;   // quad_perm
+constexpr int kMirror8 = 0x141, kMirror16 = 0x140;                    // row_half_mirror, row_mirror
+template <int J>
+__device__ __forceinline__ uint32_t lane_xor(uint32_t x) {
+  if constexpr (J == 1) {
+    return dpp<kQuadXor1>(x);
+  } else if constexpr (J == 2) {
+    return dpp<kQuadXor2>(x);
+  } else if constexpr (J == 4) {
+    return dpp<kQuadXor3>(dpp<kMirror8>(x));
+  } else if constexpr (J == 8) {
+    return dpp<kMirror8>(dpp<kMirror16>(x));
+  } else if constexpr (J == 16) {
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    return (threadIdx.x & 16) ? r[0] : r[1];
+  } else {
+    return swap_halves(x);
+  }
+}
+template <int J>
+__device__ __forceinline__ u64 compare_exchange(u64 x, bool keep_max) {
+  const u64 y = ((u64)lane_xor<J>((uint32_t)(x >> 32)) << 32) | lane_xor<J>((uint32_t)x);
   return (x > y) == keep_max ? x : y;
 }
+template <int J>
+__device__ __forceinline__ uint32_t compare_exchange(uint32_t x, bool keep_max) {
+  const uint32_t y = lane_xor<J>(x);
+  return keep_max ? max(x, y) : min(x, y);
+}
+// One bitonic merge of runs of K lanes, descending where `down`.
+template <int K, class Key>
+__device__ __forceinline__ Key bitonic(Key x, bool down) {
+  const int lane = threadIdx.x & 63;
+  if constexpr (K >= 64) x = compare_exchange<32>(x, ((lane & 32) == 0) == down);
+  if constexpr (K >= 32) x = compare_exchange<16>(x, ((lane & 16) == 0) == down);
+  if constexpr (K >= 16) x = compare_exchange<8>(x, ((lane & 8) == 0) == down);
+  if constexpr (K >= 8) x = compare_exchange<4>(x, ((lane & 4) == 0) == down);
+  if constexpr (K >= 4) x = compare_exchange<2>(x, ((lane & 2) == 0) == down);
+  return compare_exchange<1>(x, ((lane & 1) == 0) == down);
+}
+// Sorted over the wave's lanes, descending where `down`.
+template <class Key>
+__device__ __forceinline__ Key sort_lanes(Key x, bool down) {
+  const int lane = threadIdx.x & 63;
+  x = bitonic<2>(x, ((lane & 2) != 0) != down);
+  x = bitonic<4>(x, ((lane & 4) != 0) != down);
+  x = bitonic<8>(x, ((lane & 8) != 0) != down);
+  x = bitonic<16>(x, ((lane & 16) != 0) != down);
+  x = bitonic<32>(x, ((lane & 32) != 0) != down);
+  return bitonic<64>(x, down);
+}
 
-// A wave's best 64 keys, lane i the i-th (0: none).
+// Places for keys that wait: fewer than 64, and two runs of every lane.
+constexpr int kBuf = 64 + 64 * 2;
+
+// Keys of a wave that may be among the n_top best of its elements: some wait,
+// unsorted, in LDS; once 64 do they are merged into a sorted list of 64 (lane i
+// the i-th best, 0: none).
 struct BestKeys {
   u64 best;
-  u64 thr_key;   // the n_top-th best key so far
+  u64 thr_key;   // a key below which nothing is among the n_top best
   float thr;     // its value (-inf while there is none)
-  int count;     // keys waiting in buf (below 64 between calls)
-  u64* buf;      // this wave's 128 places in LDS
+  int count;     // keys waiting in buf (below 64 between groups)
+  bool merged;   // whether best holds any
+  u64* buf;      // this wave's kBuf places in LDS
 };
 
 __device__ __forceinline__ BestKeys no_keys(u64* buf) {
-  return BestKeys{0, 0, -INFINITY, 0, buf};
+  return BestKeys{0, 0, -INFINITY, 0, false, buf};
 }
 
-// Merges 64 more keys (0: none), one per lane.
-__device__ __forceinline__ void merge_keys(BestKeys& b, u64 x, int n_top) {
-  const int lane = threadIdx.x & 63;
-  // ascending bitonic sort
-#pragma unroll
-  for (int k = 2; k <= 64; k <<= 1) {
-#pragma unroll
-    for (int j = k >> 1; j > 0; j >>= 1)
-      x = compare_exchange(x, j, ((lane & j) == 0) != ((lane & k) == 0));
-  }
+// Merges 64 more keys (0: none), ascending over the lanes.
+__device__ __forceinline__ void merge_sorted(BestKeys& b, u64 x, int n_top) {
   // descending against ascending: the larger of each pair are the best 64
-  b.best = b.best > x ? b.best : x;
-#pragma unroll
-  for (int j = 32; j > 0; j >>= 1) b.best = compare_exchange(b.best, j, (lane & j) == 0);
+  b.best = bitonic<64>(b.best > x ? b.best : x, true);
   const uint32_t lo = __shfl((uint32_t)b.best, n_top - 1);
   const uint32_t hi = __shfl((uint32_t)(b.best >> 32), n_top - 1);
-  b.thr_key = ((u64)hi << 32) | lo;
-  b.thr = b.thr_key ? key_value(b.thr_key) : -INFINITY;
+  const u64 key = ((u64)hi << 32) | lo;
+  if (key > b.thr_key) {
+    b.thr_key = key;
+    b.thr = key_value(key);
+  }
+  b.merged = true;
 }
 
-__device__ __forceinline__ void flush_keys(BestKeys& b, int n_top) {
-  const int lane = threadIdx.x & 63;
+// LDS writes of this wave's lanes before, their reads after.
+__device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
   __builtin_amdgcn_wave_barrier();
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-  const u64 x = lane < b.count ? b.buf[lane] : 0;
-  const bool more = 64 + lane < b.count;
-  const u64 y = more ? b.buf[64 + lane] : 0;
-  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-  __builtin_amdgcn_wave_barrier();
-  if (more) b.buf[lane] = y;
-  b.count = b.count > 64 ? b.count - 64 : 0;
-  merge_keys(b, x, n_top);
 }
 
-// One element per lane (every lane of the wave calls this).
-__device__ __forceinline__ void offer(BestKeys& b, float x, uint32_t idx, bool take, int n_top) {
-  const u64 key = order_key(x, idx);
-  const bool pass = take && x > -INFINITY && key > b.thr_key;
-  const u64 mask = __ballot(pass);
-  if (mask == 0) return;
+// Merges the keys that wait, 64 at a time from the end, until fewer than `keep`.
+__device__ __forceinline__ void flush_keys(BestKeys& b, int keep, int n_top) {
   const int lane = threadIdx.x & 63;
-  if (pass) b.buf[b.count + __popcll(mask & ((u64(1) << lane) - 1))] = key;
-  b.count += __popcll(mask);
-  if (b.count >= 64) flush_keys(b, n_top);
+  wave_sync();
+#pragma unroll 1
+  while (b.count >= keep) {
+    const int at = b.count > 64 ? b.count - 64 : 0;
+    const u64 x = at + lane < b.count ? b.buf[at + lane] : 0;
+    b.count = at;
+    if (__ballot(x > b.thr_key) != 0) merge_sorted(b, sort_lanes(x, false), n_top);
+  }
+  wave_sync();
 }
 
-// A group of G elements per lane from index idx; gmax its maximum.
-template <int G>
-__device__ __forceinline__ void offer_group(BestKeys& b, const float* z, float gmax, uint32_t idx,
-                                            bool first, int n_top) {
-  int own = -1;   // the element already offered
-  if (first) {
-    // (the first of equal maxima, so the one with the lowest index)
-#pragma unroll
-    for (int e = G - 1; e >= 0; --e) own = z[e] == gmax ? e : own;
-    offer(b, gmax, idx + (uint32_t)(own < 0 ? 0 : own), own >= 0, n_top);
-    if (b.count > 0) flush_keys(b, n_top);
+// Lets one key per lane wait (every lane of the wave calls this).
+__device__ __forceinline__ void append(BestKeys& b, u64 key, bool take) {
+  const bool pass = take && key >= b.thr_key;
+  const u64 mask = __ballot(pass);
+  if (pass) b.buf[b.count + __popcll(mask & ((u64(1) << (threadIdx.x & 63)) - 1))] = key;
+  b.count += __popcll(mask);
+}
+
+// A threshold from one value per lane (x: order-preserving bits, 0: none), each
+// that of an element of its own: at least n_top elements are not below the
+// n_top-th largest.
+__device__ __forceinline__ void first_threshold(BestKeys& b, uint32_t x, int n_top) {
+  const uint32_t v = __shfl(sort_lanes(x, true), n_top - 1);
+  if (v != 0) {
+    b.thr_key = (u64)v << 32;      // (any index)
+    b.thr = key_value(b.thr_key);
   }
+}
+
+// The runs of a lane's group (GT::kRun neighbours each), keyed by their largest
+// logit and first column.
+template <class GT>
+__device__ __forceinline__ void offer_group(BestKeys& b, const float* z, int64_t col, bool first,
+                                            int n_top) {
+  constexpr int kRuns = GT::G / GT::kRun;
+  float top[kRuns];
+  float gmax = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < kRuns; ++i) {
+    top[i] = z[GT::kRun * i];
+#pragma unroll
+    for (int e = 1; e < GT::kRun; ++e) top[i] = fmaxf(top[i], z[GT::kRun * i + e]);
+    gmax = fmaxf(gmax, top[i]);
+  }
+  if (first)
+    first_threshold(b, gmax > -INFINITY ? (uint32_t)(order_key(gmax, 0) >> 32) : 0, n_top);
   // Elements of later groups have larger indices than all before them, so an
   // equal value does not pass; inside a group the keys decide.
   if (__ballot(first ? gmax > -INFINITY : gmax > b.thr) == 0) return;
 #pragma unroll
-  for (int e = 0; e < G; ++e) offer(b, z[e], idx + e, e != own, n_top);
+  for (int i = 0; i < kRuns; ++i)
+    append(b, order_key(top[i], (uint32_t)GT::column(col, GT::kRun * i)),
+           top[i] > -INFINITY && (first || top[i] > b.thr));
+  if (b.count >= 64) flush_keys(b, 64, n_top);
+}
+
+// From the n_top best runs of a row (b.best) its n_top best tokens.
+template <class GT, class T>
+__device__ __forceinline__ void best_tokens(BestKeys& b, const T* z, int V, int n_top) {
+  const int lane = threadIdx.x & 63;
+  const u64 runs = b.best;
+  const int n = __popcll(__ballot(lane < n_top && runs != 0));
+  BestKeys t = no_keys(b.buf);
+  // (n_top runs have a token not below the last one's best)
+  if (n == n_top)
+    t.thr_key = (u64)__shfl((uint32_t)(runs >> 32), n_top - 1) << 32;
+  for (int i = 0; i < n * GT::kRun; i += 64) {
+    const int r = (i + lane) / GT::kRun;
+    const uint32_t lo = __shfl((uint32_t)runs, r & 63);
+    const int64_t col = (int64_t)(0xFFFFFFFFu - lo) + (i + lane) % GT::kRun;
+    const bool in = r < n && col < V;
+    const float x = in ? GT::one(z, col) : -INFINITY;
+    append(t, order_key(x, (uint32_t)col), x > -INFINITY);
+    if (t.count >= 64) flush_keys(t, 64, n_top);
+  }
+  flush_keys(t, 1, n_top);
+  b.best = t.best;
 }
 
 // ---------------------------------------------------------------- loads
-// The 16-byte group at column `col`; columns past V read as -inf.
+// Eight elements of a lane: a wave covers 512 consecutive columns from `col`
+// (the wave's first) with whole 16-byte loads.  bf16: one load, columns col + 8
+// lane + e.  fp32: two, columns col + 4 lane + e and 256 further.
 template <class T>
 struct Group;
 template <>
 struct Group<uint16_t> {
   static constexpr int G = 8;
-  static __device__ __forceinline__ void load(const uint16_t* row, int64_t col, int V, float* z) {
-    if (col + G <= V) {
-      const u32x4 v = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(row + col));
+  static constexpr int kRun = 8;   // neighbouring columns
+  struct Raw {
+    u32x4 v;
+  };
+  static __device__ __forceinline__ int64_t column(int64_t col, int e) {
+    return col + 8 * (int)(threadIdx.x & 63) + e;
+  }
+  // The elements where the group is whole (zeros else), for values(), which reads
+  // a group cut off at `end` one by one; columns past it are -inf.
+  static __device__ __forceinline__ Raw fetch(const uint16_t* row, int64_t col, int64_t end) {
+    const int64_t at = column(col, 0);
+    if (at + 8 > end) return Raw{u32x4{0, 0, 0, 0}};
+    return Raw{__builtin_nontemporal_load(reinterpret_cast<const u32x4*>(row + at))};
+  }
+  static __device__ __forceinline__ void values(const Raw& r, const uint16_t* row, int64_t col,
+                                                int64_t end, float* z) {
 #pragma unroll
-      for (int p = 0; p < 4; ++p) {
-        z[2 * p] = bf16_lo(v[p]);
-        z[2 * p + 1] = bf16_hi(v[p]);
-      }
-    } else {
+    for (int p = 0; p < 4; ++p) {
+      z[2 * p] = bf16_lo(r.v[p]);
+      z[2 * p + 1] = bf16_hi(r.v[p]);
+    }
+    const int64_t at = column(col, 0);
+    if (at + 8 > end) {
 #pragma unroll
-      for (int e = 0; e < G; ++e) z[e] = col + e < V ? bf16_to_f32(row[col + e]) : -INFINITY;
+      for (int e = 0; e < 8; ++e) z[e] = at + e < end ? bf16_to_f32(row[at + e]) : -INFINITY;
     }
   }
-  static __device__ __forceinline__ void store(uint16_t* row, int64_t col, int V, const float* z) {
-    if (col + G <= V) {
+  static __device__ __forceinline__ void store(uint16_t* row, int64_t col, int64_t end,
+                                               const float* z) {
+    const int64_t at = column(col, 0);
+    if (at + 8 <= end) {
       u32x4 v;
 #pragma unroll
       for (int p = 0; p < 4; ++p) v[p] = pack_bf16x2(z[2 * p], z[2 * p + 1]);
-      __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(row + col));
+      __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(row + at));
     } else {
 #pragma unroll
-      for (int e = 0; e < G; ++e)
-        if (col + e < V) row[col + e] = f32_to_bf16(z[e]);
+      for (int e = 0; e < 8; ++e)
+        if (at + e < end) row[at + e] = f32_to_bf16(z[e]);
     }
   }
   static __device__ __forceinline__ float one(const uint16_t* row, int64_t col) {
@@ -236,29 +385,58 @@ struct Group<uint16_t> {
 };
 template <>
 struct Group<float> {
-  static constexpr int G = 4;
-  static __device__ __forceinline__ void load(const float* row, int64_t col, int V, float* z) {
-    if (col + G <= V) {
-      const f32x4 v = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(row + col));
+  static constexpr int G = 8;
+  static constexpr int kRun = 4;
+  struct Raw {
+    f32x4 v[2];
+  };
+  static __device__ __forceinline__ int64_t column(int64_t col, int e) {
+    return col + 4 * (int)(threadIdx.x & 63) + (e & 3) + 256 * (e >> 2);
+  }
+  static __device__ __forceinline__ Raw fetch(const float* row, int64_t col, int64_t end) {
+    Raw r;
 #pragma unroll
-      for (int e = 0; e < G; ++e) z[e] = v[e];
-    } else {
+    for (int i = 0; i < 2; ++i) {
+      const int64_t at = column(col, 4 * i);
+      r.v[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (at + 4 <= end)
+        r.v[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(row + at));
+    }
+    return r;
+  }
+  static __device__ __forceinline__ void values(const Raw& r, const float* row, int64_t col,
+                                                int64_t end, float* z) {
 #pragma unroll
-      for (int e = 0; e < G; ++e) z[e] = col + e < V ? row[col + e] : -INFINITY;
+    for (int i = 0; i < 2; ++i) {
+      const int64_t at = column(col, 4 * i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) z[4 * i + e] = r.v[i][e];
+      if (at + 4 > end) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) z[4 * i + e] = at + e < end ? row[at + e] : -INFINITY;
+      }
     }
   }
-  static __device__ __forceinline__ void store(float* row, int64_t col, int V, const float* z) {
-    if (col + G <= V) {
-      const f32x4 v = {z[0], z[1], z[2], z[3]};
-      __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(row + col));
-    } else {
+  static __device__ __forceinline__ void store(float* row, int64_t col, int64_t end,
+                                               const float* z) {
 #pragma unroll
-      for (int e = 0; e < G; ++e)
-        if (col + e < V) row[col + e] = z[e];
+    for (int i = 0; i < 2; ++i) {
+      const int64_t at = column(col, 4 * i);
+      if (at + 4 <= end) {
+        const f32x4 v = {z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]};
+        __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(row + at));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (at + e < end) row[at + e] = z[4 * i + e];
+      }
     }
   }
   static __device__ __forceinline__ float one(const float* row, int64_t col) { return row[col]; }
 };
+
+constexpr int kWaveCols = 512;                    // columns of a wave's group
+constexpr int64_t kStepCols = kWaves * kWaveCols;  // of a work-group's
 
 // ---------------------------------------------------------------- results of a row
 __device__ __forceinline__ bool left_out(const LogprobArgs& a, int64_t row) {
@@ -267,27 +445,36 @@ __device__ __forceinline__ bool left_out(const LogprobArgs& a, int64_t row) {
   return t < 0 || t >= a.vocab;
 }
 
+// log p of logit z in a row with state st.  (In units of log2 a logit at the
+// type's lowest value would overflow.)
+__device__ __forceinline__ float log_p(float z, const State& st, float l2t, float tau) {
+  const float d = kLn2 * exponent(z, st.m, st.m * l2t, l2t);
+  return (isfinite(d) ? d : (z - st.m) / tau) - logf(st.s);
+}
 // By one thread of the row.
 template <class T>
-__device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, const State& st) {
-  const float inv_tau = 1.0f / a.tau;
+__device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, const State& st,
+                                          float l2t) {
   const float ln_s = logf(st.s);
-  if (a.lse) a.lse[row] = st.m / a.tau + ln_s;
+  const float mc = st.m * l2t;
+  if (a.lse) {
+    // (the weights are off by the rounding of mc, all alike)
+    const float off = isfinite(mc) ? kLn2 * fmaf(st.m, l2t, -mc) : 0.0f;
+    a.lse[row] = st.m / a.tau + (ln_s - off);
+  }
   if (a.entropy) a.entropy[row] = ln_s - kLn2 * (st.u / st.s);
   if (a.logp) {
-    const float zt =
-        Group<T>::one(static_cast<const T*>(a.z) + row * a.ld, a.target[row]);
-    a.logp[row] = (zt - st.m) * inv_tau - ln_s;
+    const float zt = Group<T>::one(static_cast<const T*>(a.z) + row * a.ld, a.target[row]);
+    a.logp[row] = log_p(zt, st, l2t, a.tau);
   }
 }
 // By the lanes of one wave of the row.
 __device__ __forceinline__ void write_keys(const LogprobArgs& a, int64_t row, const State& st,
-                                           u64 key) {
+                                           float l2t, u64 key) {
   const int lane = threadIdx.x & 63;
   if (lane >= a.n_top) return;
   a.top_idx[row * a.n_top + lane] = key ? key_index(key) : -1;
-  a.top_logp[row * a.n_top + lane] =
-      key ? (key_value(key) - st.m) * (1.0f / a.tau) - logf(st.s) : -INFINITY;
+  a.top_logp[row * a.n_top + lane] = key ? log_p(key_value(key), st, l2t, a.tau) : -INFINITY;
 }
 __device__ __forceinline__ void write_left_out(const LogprobArgs& a, int64_t row) {
   if (threadIdx.x == 0) {
@@ -309,9 +496,10 @@ __global__ __launch_bounds__(kThreads) void logprob_rows_kernel(LogprobArgs a, i
                                                                 int64_t piece,
                                                                 float* __restrict__ states,
                                                                 u64* __restrict__ keys) {
-  constexpr int G = Group<T>::G;
+  typedef Group<T> GT;
   __shared__ State wst[kWaves];
-  __shared__ u64 wbuf[TOP ? kWaves * 128 : 1];
+  __shared__ int waiting[kWaves];
+  __shared__ u64 wbuf[TOP ? kWaves * kBuf : 1];
   const int wave = threadIdx.x >> 6;
   const int lane = threadIdx.x & 63;
   const float l2t = kLog2e / a.tau;
@@ -327,40 +515,78 @@ __global__ __launch_bounds__(kThreads) void logprob_rows_kernel(LogprobArgs a, i
     const int64_t c0 = sp * piece;
     const int64_t c1 = c0 + piece < a.vocab ? c0 + piece : a.vocab;
     State st{kMinFloat, 0.0f, 0.0f};
-    BestKeys bk = no_keys(wbuf + (TOP ? wave * 128 : 0));
+    float mc = st.m * l2t;
+    BestKeys bk = no_keys(wbuf + (TOP ? wave * kBuf : 0));
     bool first = true;
-    // (whole waves stay in the loop: a wave's first column decides)
-    for (int64_t c = c0 + (int64_t)wave * 64 * G; c < c1; c += (int64_t)kThreads * G) {
-      const int64_t col = c + lane * G;
-      float v[G];
-      Group<T>::load(z, col < c1 ? col : c1, (int)c1, v);
-      float gmax = v[0];
+    // Whole waves stay in the loop (a wave's first column decides); kDeep groups
+    // are loaded ahead of their use.
+    constexpr int kDeep = 2;
+    const int64_t wc = c0 + wave * kWaveCols;
+    typename GT::Raw raw[kDeep];
 #pragma unroll
-      for (int e = 1; e < G; ++e) gmax = fmaxf(gmax, v[e]);
-      add_group<G>(st, v, gmax, l2t);
-      if constexpr (TOP) {
-        offer_group<G>(bk, v, gmax, (uint32_t)col, first, a.n_top);
-        first = false;
+    for (int i = 0; i < kDeep; ++i)
+      if (wc + i * kStepCols < c1) raw[i] = GT::fetch(z, wc + i * kStepCols, c1);
+    for (int64_t cc = wc; cc < c1; cc += kDeep * kStepCols) {
+#pragma unroll
+      for (int i = 0; i < kDeep; ++i) {
+        const int64_t c = cc + i * kStepCols;
+        if (c >= c1) break;
+        float v[GT::G];
+        GT::values(raw[i], z, c, c1, v);
+        if (c + kDeep * kStepCols < c1) raw[i] = GT::fetch(z, c + kDeep * kStepCols, c1);
+        add_group<GT::G>(st, mc, v, l2t);
+        if constexpr (TOP) {
+          offer_group<GT>(bk, v, c, first, a.n_top);
+          first = false;
+        }
       }
     }
     st = wave_state(st, l2t);
-    if constexpr (TOP) {
-      if (bk.count > 0) flush_keys(bk, a.n_top);
+    if (lane == 0) {
+      wst[wave] = st;
+      // (64 stands for more than fit one sort)
+      if constexpr (TOP) waiting[wave] = bk.merged ? 64 : bk.count;
     }
-    if (lane == 0) wst[wave] = st;
-    if constexpr (TOP) wbuf[wave * 128 + lane] = bk.best;
     __syncthreads();
+    bool few = true;
+    if constexpr (TOP) {
+      int total = 0;
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) total += waiting[w] + (waiting[w] >= 64 ? 64 : 0);
+      few = total <= 64;
+      if (!few) {
+        flush_keys(bk, 1, a.n_top);
+        wbuf[wave * kBuf + lane] = bk.best;
+        __syncthreads();
+      }
+    }
     if (wave == 0) {
       State t = wst[0];
 #pragma unroll
       for (int w = 1; w < kWaves; ++w) t = merge_states(t, wst[w], l2t);
       if constexpr (TOP) {
+        if (few) {
+          // all waves' keys fit the lanes of one
+          u64 x = 0;
+          int at = lane;
+#pragma unroll
+          for (int w = 0; w < kWaves; ++w) {
+            if (at >= 0 && at < waiting[w]) x = wbuf[w * kBuf + at];
+            at -= waiting[w];
+          }
+          bk.best = sort_lanes(x, true);
+        } else {
 #pragma unroll 1
-        for (int w = 1; w < kWaves; ++w) merge_keys(bk, wbuf[w * 128 + lane], a.n_top);
+          for (int w = 1; w < kWaves; ++w)
+            merge_sorted(bk, wbuf[w * kBuf + 63 - lane], a.n_top);
+        }
       }
       if (n_split == 1) {
-        if (lane == 0) write_row<T>(a, row, t);
-        if constexpr (TOP) write_keys(a, row, t, bk.best);
+        if (lane == 0) write_row<T>(a, row, t, l2t);
+        if constexpr (TOP) {
+          best_tokens<GT>(bk, z, a.vocab, a.n_top);
+          write_keys(a, row, t, l2t, bk.best);
+        }
       } else {
         if (lane == 0) {
           states[3 * task] = t.m;
@@ -381,7 +607,7 @@ template <class T, bool TOP>
 __global__ __launch_bounds__(64) void logprob_join_kernel(LogprobArgs a, int n_split,
                                                           const float* __restrict__ states,
                                                           const u64* __restrict__ keys) {
-  __shared__ u64 buf[TOP ? 128 : 1];
+  __shared__ u64 buf[TOP ? kBuf : 1];
   const int lane = threadIdx.x;
   const float l2t = kLog2e / a.tau;
   for (int64_t row = blockIdx.x; row < a.n_tok; row += gridDim.x) {
@@ -392,44 +618,48 @@ __global__ __launch_bounds__(64) void logprob_join_kernel(LogprobArgs a, int n_s
       st = merge_states(st, State{q[0], q[1], q[2]}, l2t);
     }
     st = wave_state(st, l2t);
-    if (lane == 0) write_row<T>(a, row, st);
+    if (lane == 0) write_row<T>(a, row, st, l2t);
     if constexpr (TOP) {
       BestKeys bk = no_keys(buf);
+      // the pieces' best keys first: their n_top-th leaves few others
+      const u64* q = keys + row * n_split * a.n_top;
+      first_threshold(bk, lane < n_split ? (uint32_t)(q[lane * a.n_top] >> 32) : 0, a.n_top);
       const int n = n_split * a.n_top;
-      const u64* q = keys + row * n;
       for (int i = 0; i < n; i += 64) {
         const u64 x = i + lane < n ? q[i + lane] : 0;
-        if (__ballot(x > bk.thr_key) != 0) merge_keys(bk, x, a.n_top);
+        append(bk, x, x != 0);
+        if (bk.count >= 64) flush_keys(bk, 64, a.n_top);
       }
-      write_keys(a, row, st, bk.best);
+      flush_keys(bk, 1, a.n_top);
+      best_tokens<Group<T>>(bk, static_cast<const T*>(a.z) + row * a.ld, a.vocab, a.n_top);
+      write_keys(a, row, st, l2t, bk.best);
     }
   }
 }
 
 // dz over pieces of kGradGroups groups per thread.
 constexpr int kGradGroups = 4;
+constexpr int64_t kGradCols = kStepCols * kGradGroups;
 
 template <class T>
 __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs a, int n_pieces) {
-  constexpr int G = Group<T>::G;
-  constexpr int64_t kPiece = (int64_t)kThreads * G * kGradGroups;
+  typedef Group<T> GT;
+  constexpr int G = GT::G;
   const int64_t n_tasks = a.n_tok * n_pieces;
+  const int64_t V = a.vocab;
   // 1 / tau as two floats: z / tau keeps fp32 accuracy in one fused step
   const float ih = 1.0f / a.tau;
   const float il = fmaf(-a.tau, ih, 1.0f) / a.tau;
   for (int64_t task = blockIdx.x; task < n_tasks; task += gridDim.x) {
     const int64_t row = task / n_pieces;
-    const int64_t c0 = (task - row * n_pieces) * kPiece;
+    const int64_t c0 = (task - row * n_pieces) * kGradCols + (threadIdx.x >> 6) * kWaveCols;
     const T* z = static_cast<const T*>(a.z) + row * a.ld;
     T* dz = static_cast<T*>(a.dz) + row * a.ldz;
     const int64_t target = a.target ? a.target[row] : -1;
-    if (a.target && (target < 0 || target >= a.vocab)) {
+    if (a.target && (target < 0 || target >= V)) {
       const float zero[G] = {};
 #pragma unroll
-      for (int i = 0; i < kGradGroups; ++i) {
-        const int64_t col = c0 + ((int64_t)i * kThreads + threadIdx.x) * G;
-        if (col < a.vocab) Group<T>::store(dz, col, a.vocab, zero);
-      }
+      for (int i = 0; i < kGradGroups; ++i) GT::store(dz, c0 + i * kStepCols, V, zero);
       continue;
     }
     const float lse = a.lse[row];
@@ -439,33 +669,31 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
     const float H = a.d_entropy ? a.entropy[row] : 0.0f;
     // dz_j = p_j (k0 + k1 log p_j) + [j = target] kt
     const float k0 = (gl - g - gh * H) * ih, k1 = -gh * ih, kt = g * ih;
-    float v[kGradGroups][G];
+    typename GT::Raw raw[kGradGroups];
+#pragma unroll
+    for (int i = 0; i < kGradGroups; ++i) raw[i] = GT::fetch(z, c0 + i * kStepCols, V);
 #pragma unroll
     for (int i = 0; i < kGradGroups; ++i) {
-      const int64_t col = c0 + ((int64_t)i * kThreads + threadIdx.x) * G;
-      if (col < a.vocab) Group<T>::load(z, col, a.vocab, v[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kGradGroups; ++i) {
-      const int64_t col = c0 + ((int64_t)i * kThreads + threadIdx.x) * G;
-      if (col >= a.vocab) continue;
+      const int64_t c = c0 + i * kStepCols;
+      float v[G];
+      GT::values(raw[i], z, c, V, v);
 #pragma unroll
       for (int e = 0; e < G; ++e) {
-        const float lp = fmaf(v[i][e], ih, fmaf(v[i][e] == -INFINITY ? 0.0f : v[i][e], il, -lse));
+        const float lp = fmaf(v[e], ih, fmaf(v[e] == -INFINITY ? 0.0f : v[e], il, -lse));
         const float p = exp2_normal(lp * kLog2e);
         // (a masked token: p = 0 and log p kept finite)
         float o = p * fmaf(k1, fmaxf(lp, kLow), k0);
-        if (col + e == target) o += kt;
-        v[i][e] = o;
+        if (GT::column(c, e) == target) o += kt;
+        v[e] = o;
       }
-      Group<T>::store(dz, col, a.vocab, v[i]);
+      GT::store(dz, c, V, v);
     }
   }
 }
 
 // Work-groups a chip full of streaming work wants, and the most a launch takes
 // (tasks beyond it are walked by the same work-groups).
-constexpr int64_t kFill = 1024;
+constexpr int64_t kFill = 512;
 constexpr int64_t kMaxGrid = 1 << 20;
 
 template <class T>
@@ -493,8 +721,7 @@ hipError_t launch_rows(const LogprobArgs& a, const LogprobPlan& p, char* ws, hip
 
 template <class T>
 hipError_t launch_grad(const LogprobGradArgs& a, hipStream_t s) {
-  constexpr int64_t kPiece = (int64_t)kThreads * Group<T>::G * kGradGroups;
-  const int n_pieces = (int)((a.vocab + kPiece - 1) / kPiece);
+  const int n_pieces = (int)((a.vocab + kGradCols - 1) / kGradCols);
   const int64_t tasks = a.n_tok * n_pieces;
   hipLaunchKernelGGL((logprob_grad_kernel<T>), dim3((unsigned)(tasks < kMaxGrid ? tasks : kMaxGrid)),
                      dim3(kThreads), 0, s, a, n_pieces);
@@ -505,15 +732,13 @@ hipError_t launch_grad(const LogprobGradArgs& a, hipStream_t s) {
 
 LogprobPlan make_logprob_plan(int64_t n_tok, int64_t vocab, int n_top) {
   LogprobPlan p{};
-  // whole steps of a bf16 work-group (2048 columns) per piece, and no more
-  // pieces than fill the chip
-  constexpr int64_t kStep = (int64_t)kThreads * 8;
-  const int64_t steps = (vocab + kStep - 1) / kStep;
+  // whole steps of a work-group per piece, and no more pieces than fill the chip
+  const int64_t steps = (vocab + kStepCols - 1) / kStepCols;
   int64_t want = n_tok > 0 ? (kFill + n_tok - 1) / n_tok : 1;
   if (want > steps) want = steps;
   if (want < 1) want = 1;
   const int64_t per = (steps + want - 1) / want;
-  p.piece = per * kStep;
+  p.piece = per * kStepCols;
   p.n_split = (int)((steps + per - 1) / per);
   if (p.n_split > 1) {
     p.off_keys = (size_t)round_up(n_tok * p.n_split * 12, 256);
