@@ -104,7 +104,7 @@ int logra_token_logprob_backward(const void* z, int dtype, int64_t n_tok, int64_
 /* Entries of an 8-bit state block, which share one exponent byte. */
 #define LOGRA_STATE_BLOCK 32
 
-/* One tensor of logra_adamw_step, n entries each. */
+/* One tensor of an AdamW step, n entries in each array. */
 typedef struct logra_adamw_item {
   void* p;             /* weights, in/out: p_type */
   const void* g;       /* gradient: g_type */
@@ -119,8 +119,26 @@ typedef struct logra_adamw_item {
   int32_t g_type;      /* LOGRA_BF16 or LOGRA_F32 */
 } logra_adamw_item;
 
+/* Bytes of a table of n tensors (0 for n < 0 or n > 2^24). */
+size_t logra_adamw_table_bytes(int32_t n);
+
 /*
- * logra_adamw_step - one AdamW step over n tensors:
+ * logra_adamw_table - checks n tensors and lays them out for logra_adamw_step:
+ * a host function, no HIP call.  A program makes the table once and again when
+ * an array moves (the table holds addresses), and copies its bytes to device
+ * memory.
+ * items: host array of n entries, 0 <= n <= 2^24 (tensors with n == 0 entries are
+ *     left out).  p, g, master, m, v aligned to their types; weight_decay
+ *     finite.  No array that is written may overlap another (not checked).
+ * table: host memory of logra_adamw_table_bytes(n) bytes, 8-B aligned, written.
+ * Returns LOGRA_OK, LOGRA_EINVAL (also past 2^24 work-groups of one form, about
+ * 6 10^10 entries) or LOGRA_EWORKSPACE (bytes too few).
+ */
+int logra_adamw_table(int32_t n, const logra_adamw_item* items, void* table, size_t bytes);
+
+/*
+ * logra_adamw_step - one AdamW step over the tensors of a table, one launch for
+ * each form among them (weights, gradient and state types):
  *   g' = g grad_scale            (grad_scale: device float, NULL for 1)
  *   m <- beta1 m + (1 - beta1) g'
  *   v <- beta2 v + (1 - beta2) g'^2
@@ -152,16 +170,15 @@ typedef struct logra_adamw_item {
  *   equally spaced values, so that states move by less than a rounding step on
  *   average as they should; rounded to nearest, a v with beta2 = 0.999 stays
  *   where it is (0.1 % of a step against a spacing of 6 %).
- *   Zeroed codes with any E are the zero state.
+ *   Zeroed codes with any E below 255 are the zero state.
  *
- * items: host array of n entries, n >= 0 (0: a no-op); tensors with n == 0
- *     entries are left out.  p, g, master, m, v aligned to their types.  No
- *     array that is written may overlap another (not checked).
- * lr, beta1, beta2, eps finite; beta in [0, 1); lr, eps >= 0; step >= 1;
- *     weight_decay finite.
+ * table: host memory as logra_adamw_table left it; table_dev: device copy of the
+ *     same bytes, 8-B aligned (not inspected when there is nothing to do).
+ * lr, beta1, beta2, eps finite; beta in [0, 1) as a float; lr, eps >= 0; step >=
+ *     1.
  * Returns LOGRA_OK, LOGRA_EINVAL or LOGRA_EHIP.
  */
-int logra_adamw_step(int32_t n, const logra_adamw_item* items, double lr, double beta1,
+int logra_adamw_step(const void* table, const void* table_dev, double lr, double beta1,
                      double beta2, double eps, int64_t step, const float* grad_scale,
                      hipStream_t s);
 

@@ -130,8 +130,9 @@ SIGNATURES.update({
     "logra_token_logprob_backward": (ctypes.c_int, [c_vp, ctypes.c_int, _i64, _i64, _i64, c_vp,
                                                     _f32, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, _i64,
                                                     c_vp]),
-    "logra_adamw_step": (ctypes.c_int, [_i32, ctypes.POINTER(AdamWItem), _f64, _f64, _f64, _f64,
-                                        _i64, c_vp, c_vp]),
+    "logra_adamw_table_bytes": (_sz, [_i32]),
+    "logra_adamw_table": (ctypes.c_int, [_i32, ctypes.POINTER(AdamWItem), c_vp, _sz]),
+    "logra_adamw_step": (ctypes.c_int, [c_vp, c_vp, _f64, _f64, _f64, _f64, _i64, c_vp, c_vp]),
     "logra_adamw_state_values": (ctypes.c_int, [ctypes.c_int, c_vp, c_vp, _i64, c_vp, c_vp]),
     "logra_adapter_ws_bytes": (_sz, [_i64, _i64, _i64, _i32]),
     "logra_adapter_apply": (ctypes.c_int, [c_vp, _i64, c_vp, _i64, c_vp, _i64, _i64, _i64, _i64,

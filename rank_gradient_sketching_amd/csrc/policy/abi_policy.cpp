@@ -5,6 +5,7 @@
 #include "logra_policy.h"
 
 #include <math.h>
+#include <string.h>
 
 #include "internal.hpp"
 #include "policy/internal_policy.hpp"
@@ -43,6 +44,15 @@ Span span(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t elem) {
 bool overlap(const Span& a, const Span& b) {
   return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi;
 }
+
+// The table of an AdamW step: its head, the items, their first work-groups.
+constexpr uint64_t kTableMagic = 0x57414D4152474F4Cull;
+size_t table_bytes(int32_t n) {
+  return (size_t)logra::round_up(
+      (int64_t)sizeof(logra::AdamwTable) + (int64_t)n * ((int64_t)sizeof(logra::AdamwItem) + 4), 256);
+}
+static_assert(sizeof(logra::AdamwTable) % 8 == 0 && sizeof(logra::AdamwItem) % 8 == 0,
+              "items on 8-byte boundaries");
 
 }  // namespace
 
@@ -119,14 +129,15 @@ int logra_token_logprob_backward(const void* z, int dtype, int64_t n_tok, int64_
   return hip_status(logra::launch_token_logprob_backward(a, dtype == LOGRA_F32, s));
 }
 
-int logra_adamw_step(int32_t n, const logra_adamw_item* items, double lr, double beta1,
-                     double beta2, double eps, int64_t step, const float* grad_scale,
-                     hipStream_t s) {
-  if (n < 0 || (n > 0 && items == nullptr)) return LOGRA_EINVAL;
-  if (!isfinite(lr) || lr < 0.0 || !isfinite(eps) || eps < 0.0 || step < 1) return LOGRA_EINVAL;
-  for (const double b : {beta1, beta2})
-    if (!isfinite(b) || b < 0.0 || !((float)b < 1.0f)) return LOGRA_EINVAL;
-  if (!aligned(grad_scale, 4)) return LOGRA_EINVAL;
+size_t logra_adamw_table_bytes(int32_t n) {
+  if (n < 0 || n > (1 << 24)) return 0;
+  return table_bytes(n);
+}
+
+int logra_adamw_table(int32_t n, const logra_adamw_item* items, void* table, size_t bytes) {
+  if (n < 0 || n > (1 << 24) || (n > 0 && items == nullptr)) return LOGRA_EINVAL;
+  if (table == nullptr || !aligned(table, 8)) return LOGRA_EINVAL;
+  if (bytes < table_bytes(n)) return LOGRA_EWORKSPACE;
   for (int i = 0; i < n; ++i) {
     const logra_adamw_item& q = items[i];
     if (!type_ok(q.p_type) || !type_ok(q.g_type) || !isfinite(q.weight_decay)) return LOGRA_EINVAL;
@@ -140,6 +151,64 @@ int logra_adamw_step(int32_t n, const logra_adamw_item* items, double lr, double
         !aligned(q.master, 4) || !aligned(q.m, state8 ? 1 : 4) || !aligned(q.v, state8 ? 1 : 4))
       return LOGRA_EINVAL;
   }
+  char* const base = static_cast<char*>(table);
+  memset(base, 0, table_bytes(n));
+  logra::AdamwTable* const t = reinterpret_cast<logra::AdamwTable*>(base);
+  t->magic = kTableMagic;
+  t->bytes = table_bytes(n);
+  auto form_of = [](const logra_adamw_item& q) {
+    const int weights = q.p_type == LOGRA_F32 ? 0 : q.master == nullptr ? 1 : 2;
+    return weights * 4 + (q.g_type == LOGRA_F32 ? 2 : 0) + (q.m_exp != nullptr ? 1 : 0);
+  };
+  for (int i = 0; i < n; ++i)
+    if (items[i].n > 0) ++t->form[form_of(items[i])].n;
+  // the items of all forms, then their first work-groups
+  uint32_t at = sizeof(logra::AdamwTable);
+  for (logra::AdamwForm& f : t->form) {
+    f.off_items = at;
+    at += (uint32_t)f.n * (uint32_t)sizeof(logra::AdamwItem);
+  }
+  for (logra::AdamwForm& f : t->form) {
+    f.off_first = at;
+    at += (uint32_t)f.n * 4;
+  }
+  int32_t done[logra::kAdamwForms] = {};
+  uint32_t dither0 = 0;
+  for (int i = 0; i < n; ++i) {
+    const logra_adamw_item& x = items[i];
+    if (x.n == 0) continue;
+    const int k = form_of(x);
+    reinterpret_cast<logra::AdamwItem*>(base + t->form[k].off_items)[done[k]++] =
+        logra::AdamwItem{x.p, x.g, x.master, x.m, x.v, x.m_exp, x.v_exp, x.n, x.weight_decay,
+                         dither0, 0, 0};
+    dither0 += (uint32_t)logra::round_up(x.n, logra::kStateBlock);
+  }
+  for (int k = 0; k < logra::kAdamwForms; ++k) {
+    logra::AdamwForm& f = t->form[k];
+    if (!logra::adamw_lay_out(&f, reinterpret_cast<logra::AdamwItem*>(base + f.off_items),
+                              reinterpret_cast<int32_t*>(base + f.off_first), (k & 2) != 0,
+                              (k & 1) != 0, static_cast<logra::AdamwWeights>(k / 4))) {
+      t->magic = 0;
+      return LOGRA_EINVAL;
+    }
+  }
+  return LOGRA_OK;
+}
+
+int logra_adamw_step(const void* table, const void* table_dev, double lr, double beta1,
+                     double beta2, double eps, int64_t step, const float* grad_scale,
+                     hipStream_t s) {
+  if (table == nullptr || !aligned(table, 8)) return LOGRA_EINVAL;
+  const logra::AdamwTable& t = *static_cast<const logra::AdamwTable*>(table);
+  if (t.magic != kTableMagic) return LOGRA_EINVAL;
+  if (!isfinite(lr) || lr < 0.0 || !isfinite(eps) || eps < 0.0 || step < 1) return LOGRA_EINVAL;
+  for (const double b : {beta1, beta2})
+    if (!isfinite(b) || b < 0.0 || !((float)b < 1.0f)) return LOGRA_EINVAL;
+  if (!aligned(grad_scale, 4)) return LOGRA_EINVAL;
+  bool any = false;
+  for (const logra::AdamwForm& f : t.form) any = any || f.n > 0;
+  if (!any) return LOGRA_OK;
+  if (table_dev == nullptr || !aligned(table_dev, 8)) return LOGRA_EINVAL;
   logra::AdamwScalars h{};
   h.lr = (float)lr;
   h.b1 = (float)beta1;
@@ -151,36 +220,15 @@ int logra_adamw_step(int32_t n, const logra_adamw_item* items, double lr, double
   h.inv_sqrt_bc2 = (float)(1.0 / sqrt(1.0 - pow(beta2, (double)step)));
   h.dither_step = (uint32_t)step * logra::kDitherStep;
   h.grad_scale = grad_scale;
-  // The tensors of one variant share launches; a block of the list at a time,
-  // so that nothing is allocated.
-  constexpr int kBlock = 256;
-  uint32_t dither0 = 0;
-  for (int i0 = 0; i0 < n; i0 += kBlock) {
-    const int m = n - i0 < kBlock ? n - i0 : kBlock;
-    logra::AdamwItem q[kBlock];
-    int variant[kBlock];
-    for (int i = 0; i < m; ++i) {
-      const logra_adamw_item& x = items[i0 + i];
-      q[i] = logra::AdamwItem{x.p,     x.g,     x.master, x.m,            x.v,
-                              x.m_exp, x.v_exp, x.n,      x.weight_decay, dither0};
-      const int weights = x.p_type == LOGRA_F32 ? 0 : x.master == nullptr ? 1 : 2;
-      variant[i] =
-          weights * 4 + (x.g_type == LOGRA_F32 ? 2 : 0) + (x.m_exp != nullptr ? 1 : 0);
-      dither0 += (uint32_t)(logra::round_up(x.n, logra::kStateBlock));
-    }
-    for (int v = 0; v < 12; ++v) {
-      const logra::AdamwItem* list[kBlock];
-      int c = 0;
-      for (int i = 0; i < m; ++i)
-        if (variant[i] == v) list[c++] = &q[i];
-      if (c == 0) continue;
-      const logra::AdamwWeights w = v < 4   ? logra::AdamwWeights::kF32
-                                    : v < 8 ? logra::AdamwWeights::kBf16
-                                            : logra::AdamwWeights::kBf16Master;
-      const int st =
-          hip_status(logra::launch_adamw(w, (v & 2) != 0, (v & 1) != 0, list, c, h, s));
-      if (st != LOGRA_OK) return st;
-    }
+  const char* const dev = static_cast<const char*>(table_dev);
+  for (int k = 0; k < logra::kAdamwForms; ++k) {
+    const logra::AdamwForm& f = t.form[k];
+    if (f.n == 0) continue;
+    const int st = hip_status(logra::launch_adamw(
+        static_cast<logra::AdamwWeights>(k / 4), (k & 2) != 0, (k & 1) != 0, f,
+        reinterpret_cast<const logra::AdamwItem*>(dev + f.off_items),
+        reinterpret_cast<const int32_t*>(dev + f.off_first), h, s));
+    if (st != LOGRA_OK) return st;
   }
   return LOGRA_OK;
 }

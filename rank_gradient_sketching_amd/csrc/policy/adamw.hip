@@ -39,31 +39,12 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kVec = 4;                              // entries per lane and step
-constexpr int kSteps = 4;
-constexpr int kChunk = kThreads * kVec * kSteps;     // entries per work-group
-constexpr int kMaxItems = 48;
-
-struct Item {
-  void* p;
-  const void* g;
-  float* master;
-  void* m;
-  void* v;
-  uint8_t* m_exp;
-  uint8_t* v_exp;
-  int64_t n;
-  float weight_decay;
-  uint32_t dither0;
-  int vec;      // every array on a boundary of kVec of its entries
-  int pad;
-};
-struct Launch {
-  AdamwScalars h;
-  int n;
-  int first[kMaxItems];   // first work-group of each tensor
-  Item item[kMaxItems];
-};
-static_assert(sizeof(Launch) <= 4096, "kernel argument block");
+constexpr int kStep = kThreads * kVec;               // entries per work-group and step
+constexpr int kManySteps = 4;
+// Below this many work-groups of kManySteps steps, one step each: 140 tensors of
+// 1536 and 256 entries took the same 4 us (latency), 23 ragged ones of 640 k
+// entries with 8-bit states 11 us in 160 work-groups.
+constexpr int64_t kFew = 1024;
 
 // ---------------------------------------------------------------- 8-bit states
 constexpr int kKeepM = 3, kKeepV = 4;            // mantissa bits kept
@@ -174,37 +155,55 @@ __device__ __forceinline__ void store4(uint8_t* a, int64_t i, int64_t n, bool ve
 }
 
 // ---------------------------------------------------------------- the step
-template <AdamwWeights W, bool G32, bool S8>
-__global__ __launch_bounds__(kThreads) void adamw_kernel(const Launch L) {
+// Index of the tensor that work-group wg belongs to: the last one whose first
+// work-group is not past it.
+__device__ __forceinline__ int find_tensor(const int32_t* __restrict__ first, int n, int wg) {
+  const int lane = threadIdx.x & 63;
+  int lo = 0, len = n;
+  while (len > 1) {
+    const int step = (len + 63) / 64;
+    const int at = lane * step;
+    const int before = __popcll(__ballot(at < len && first[lo + (at < len ? at : 0)] <= wg));
+    lo += (before - 1) * step;
+    len = len - (before - 1) * step < step ? len - (before - 1) * step : step;
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
+template <AdamwWeights W, bool G32, bool S8, int kSteps>
+__global__ __launch_bounds__(kThreads) void adamw_kernel(const AdamwScalars h,
+                                                         const AdamwItem* __restrict__ items,
+                                                         const int32_t* __restrict__ first,
+                                                         int n_items) {
   typedef typename std::conditional<W == AdamwWeights::kF32, float, uint16_t>::type PT;
   typedef typename std::conditional<G32, float, uint16_t>::type GT;
   const int lane = threadIdx.x & 63;
   const int wg = (int)blockIdx.x;
-  const int mine = lane < L.n && L.first[lane < kMaxItems ? lane : 0] <= wg;
-  const int it = __builtin_amdgcn_readfirstlane(__popcll(__ballot(mine)) - 1);
-  PT* const p = static_cast<PT*>(L.item[it].p);
-  const GT* const g = static_cast<const GT*>(L.item[it].g);
-  float* const master = L.item[it].master;
-  void* const mp = L.item[it].m;
-  void* const vp = L.item[it].v;
-  uint8_t* const m_exp = L.item[it].m_exp;
-  uint8_t* const v_exp = L.item[it].v_exp;
-  const int64_t n = L.item[it].n;
-  const float wd = L.item[it].weight_decay;
-  const uint32_t d0 = L.item[it].dither0;
-  const bool vec_ok = L.item[it].vec != 0;
-  const float lr = L.h.lr, b1 = L.h.b1, b2 = L.h.b2, c1 = L.h.c1, c2 = L.h.c2, eps = L.h.eps;
-  const float ibc1 = L.h.inv_bc1, isbc2 = L.h.inv_sqrt_bc2;
-  const uint32_t dstep = L.h.dither_step;
-  const float gs = L.h.grad_scale ? *L.h.grad_scale : 1.0f;
+  const int it = find_tensor(first, n_items, wg);
+  const AdamwItem& q = items[it];
+  PT* const p = static_cast<PT*>(q.p);
+  const GT* const g = static_cast<const GT*>(q.g);
+  float* const master = q.master;
+  void* const mp = q.m;
+  void* const vp = q.v;
+  uint8_t* const m_exp = q.m_exp;
+  uint8_t* const v_exp = q.v_exp;
+  const int64_t n = q.n;
+  const float wd = q.weight_decay;
+  const uint32_t d0 = q.dither0;
+  const bool vec_ok = q.vec != 0;
+  const float lr = h.lr, b1 = h.b1, b2 = h.b2, c1 = h.c1, c2 = h.c2, eps = h.eps;
+  const float ibc1 = h.inv_bc1, isbc2 = h.inv_sqrt_bc2;
+  const uint32_t dstep = h.dither_step;
+  const float gs = h.grad_scale ? *h.grad_scale : 1.0f;
 
-  const int64_t i0 = (int64_t)(wg - L.first[it]) * kChunk + (int64_t)threadIdx.x * kVec;
+  const int64_t i0 = (int64_t)(wg - first[it]) * (kStep * kSteps) + (int64_t)threadIdx.x * kVec;
   float xw[kSteps][kVec], xg[kSteps][kVec], xm[kSteps][kVec], xv[kSteps][kVec];
   uint32_t qm[kSteps], qv[kSteps];
   int em[kSteps], ev[kSteps];
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
-    const int64_t i = i0 + (int64_t)s * kThreads * kVec;
+    const int64_t i = i0 + (int64_t)s * kStep;
     const bool vec = vec_ok && i + kVec <= n;
 #pragma unroll
     for (int e = 0; e < kVec; ++e) xw[s][e] = xg[s][e] = xm[s][e] = xv[s][e] = 0.0f;
@@ -229,7 +228,7 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Launch L) {
   }
 #pragma unroll
   for (int s = 0; s < kSteps; ++s) {
-    const int64_t i = i0 + (int64_t)s * kThreads * kVec;
+    const int64_t i = i0 + (int64_t)s * kStep;
     const bool vec = vec_ok && i + kVec <= n;
     float xr[kVec];
 #pragma unroll
@@ -287,111 +286,112 @@ __global__ __launch_bounds__(kThreads) void adamw_kernel(const Launch L) {
   }
 }
 
+// Sixteen entries (half a block) per lane: one 16-byte load, two 16-byte stores.
+constexpr int kValues = 16;
+
 template <bool SECOND>
 __global__ __launch_bounds__(kThreads) void state_values_kernel(const uint8_t* __restrict__ codes,
                                                                 const uint8_t* __restrict__ exps,
                                                                 int64_t n, bool vec_ok,
                                                                 uint16_t* __restrict__ out) {
-  const int64_t stride = (int64_t)gridDim.x * kThreads * kVec;
-  for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * kVec; i < n; i += stride) {
-    const bool vec = vec_ok && i + kVec <= n;
-    const uint32_t q = load4(codes, i, n, vec);
+  const int64_t stride = (int64_t)gridDim.x * kThreads * kValues;
+  for (int64_t i = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * kValues; i < n; i += stride) {
     const int E = exps[i / kStateBlock];
-    float x[kVec];
+    auto value = [&](uint32_t c) { return SECOND ? decode<kKeepV>(c, E) : decode_m(c, E); };
+    if (vec_ok && i + kValues <= n) {
+      const u32x4 q = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(codes + i));
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) {
-      const uint32_t c = (q >> (8 * e)) & 255u;
-      x[e] = SECOND ? decode<kKeepV>(c, E) : decode_m(c, E);
+      for (int h = 0; h < 2; ++h) {
+        u32x4 v;
+#pragma unroll
+        for (int p = 0; p < 4; ++p) {
+          const uint32_t c = q[2 * h + (p >> 1)] >> (16 * (p & 1));
+          v[p] = pack_bf16x2(value(c & 255u), value((c >> 8) & 255u));
+        }
+        __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(out + i + 8 * h));
+      }
+    } else {
+      for (int e = 0; e < kValues && i + e < n; ++e) out[i + e] = f32_to_bf16(value(codes[i + e]));
     }
-    store4(out, i, n, vec, x);
   }
 }
 
 bool on(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 template <AdamwWeights W, bool G32, bool S8>
-hipError_t launch_variant(const AdamwItem* const* items, int n, const AdamwScalars& h,
-                          hipStream_t s) {
-  constexpr int64_t kMostGroups = (int64_t(1) << 24) - 1;   // 2^32 threads less one group
-  Launch L;
-  L.h = h;
-  L.n = 0;
-  int64_t groups = 0;
-  auto flush = [&]() {
-    if (L.n == 0) return hipSuccess;
-    hipLaunchKernelGGL((adamw_kernel<W, G32, S8>), dim3((unsigned)groups), dim3(kThreads), 0, s, L);
-    L.n = 0;
-    groups = 0;
-    return hipGetLastError();
-  };
-  for (int i = 0; i < n; ++i) {
-    AdamwItem q = *items[i];
-    // a tensor past one launch's work-groups goes on in the next, at a whole
-    // number of chunks (so of blocks)
-    while (q.n > 0) {
-      const int64_t chunks = (q.n + kChunk - 1) / kChunk;
-      const int64_t room = kMostGroups - groups;
-      if (L.n == kMaxItems || room == 0) {
-        const hipError_t e = flush();
-        if (e != hipSuccess) return e;
-        continue;
-      }
-      const int64_t take = chunks <= room ? q.n : room * kChunk;
-      const size_t pb = W == AdamwWeights::kF32 ? 4 : 2, gb = G32 ? 4 : 2, sb = S8 ? 1 : 4;
-      L.first[L.n] = (int)groups;
-      L.item[L.n] = Item{q.p, q.g, q.master, q.m, q.v, q.m_exp, q.v_exp, take, q.weight_decay,
-                         q.dither0,
-                         on(q.p, kVec * pb) && on(q.g, kVec * gb) && on(q.master, kVec * 4) &&
-                                 on(q.m, kVec * sb) && on(q.v, kVec * sb)
-                             ? 1
-                             : 0,
-                         0};
-      ++L.n;
-      groups += (take + kChunk - 1) / kChunk;
-      q.p = static_cast<char*>(q.p) + take * pb;
-      q.g = static_cast<const char*>(q.g) + take * gb;
-      if (q.master) q.master += take;
-      q.m = static_cast<char*>(q.m) + take * sb;
-      q.v = static_cast<char*>(q.v) + take * sb;
-      if (S8) {
-        q.m_exp += take / kStateBlock;
-        q.v_exp += take / kStateBlock;
-      }
-      q.dither0 += (uint32_t)take;
-      q.n -= take;
-    }
-  }
-  return flush();
+void launch_form(int steps, int64_t groups, const AdamwScalars& h, const AdamwItem* items,
+                 const int32_t* first, int n, hipStream_t s) {
+  const dim3 grid((unsigned)groups), block(kThreads);
+  if (steps == 1)
+    hipLaunchKernelGGL((adamw_kernel<W, G32, S8, 1>), grid, block, 0, s, h, items, first, n);
+  else
+    hipLaunchKernelGGL((adamw_kernel<W, G32, S8, kManySteps>), grid, block, 0, s, h, items, first,
+                       n);
 }
 
 template <AdamwWeights W>
-hipError_t launch_weights(bool g_f32, bool state8, const AdamwItem* const* items, int n,
-                          const AdamwScalars& h, hipStream_t s) {
-  if (g_f32)
-    return state8 ? launch_variant<W, true, true>(items, n, h, s)
-                  : launch_variant<W, true, false>(items, n, h, s);
-  return state8 ? launch_variant<W, false, true>(items, n, h, s)
-                : launch_variant<W, false, false>(items, n, h, s);
+void launch_weights(bool g_f32, bool state8, int steps, int64_t groups, const AdamwScalars& h,
+                    const AdamwItem* items, const int32_t* first, int n, hipStream_t s) {
+  if (g_f32) {
+    if (state8)
+      launch_form<W, true, true>(steps, groups, h, items, first, n, s);
+    else
+      launch_form<W, true, false>(steps, groups, h, items, first, n, s);
+  } else {
+    if (state8)
+      launch_form<W, false, true>(steps, groups, h, items, first, n, s);
+    else
+      launch_form<W, false, false>(steps, groups, h, items, first, n, s);
+  }
 }
 
 }  // namespace
 
-hipError_t launch_adamw(AdamwWeights weights, bool g_f32, bool state8,
-                        const AdamwItem* const* items, int n, const AdamwScalars& h,
+bool adamw_lay_out(AdamwForm* form, AdamwItem* items, int32_t* first, bool g_f32, bool state8,
+                   AdamwWeights weights) {
+  int64_t groups = 0;
+  for (int i = 0; i < form->n; ++i) groups += (items[i].n + kStep * kManySteps - 1) / (kStep * kManySteps);
+  form->steps = groups < kFew ? 1 : kManySteps;
+  const int64_t chunk = (int64_t)kStep * form->steps;
+  const uintptr_t pb = weights == AdamwWeights::kF32 ? 4 : 2, gb = g_f32 ? 4 : 2;
+  const uintptr_t sb = state8 ? 1 : 4;
+  groups = 0;
+  for (int i = 0; i < form->n; ++i) {
+    AdamwItem& q = items[i];
+    q.vec = on(q.p, kVec * pb) && on(q.g, kVec * gb) && on(q.master, kVec * 4) &&
+            on(q.m, kVec * sb) && on(q.v, kVec * sb);
+    first[i] = (int32_t)groups;
+    groups += (q.n + chunk - 1) / chunk;
+    if (groups >= (int64_t(1) << 24)) return false;   // 2^32 threads
+  }
+  form->groups = (int32_t)groups;
+  return true;
+}
+
+hipError_t launch_adamw(AdamwWeights weights, bool g_f32, bool state8, const AdamwForm& form,
+                        const AdamwItem* items, const int32_t* first, const AdamwScalars& h,
                         hipStream_t s) {
   switch (weights) {
-    case AdamwWeights::kF32: return launch_weights<AdamwWeights::kF32>(g_f32, state8, items, n, h, s);
+    case AdamwWeights::kF32:
+      launch_weights<AdamwWeights::kF32>(g_f32, state8, form.steps, form.groups, h, items, first,
+                                         form.n, s);
+      break;
     case AdamwWeights::kBf16:
-      return launch_weights<AdamwWeights::kBf16>(g_f32, state8, items, n, h, s);
-    default: return launch_weights<AdamwWeights::kBf16Master>(g_f32, state8, items, n, h, s);
+      launch_weights<AdamwWeights::kBf16>(g_f32, state8, form.steps, form.groups, h, items, first,
+                                          form.n, s);
+      break;
+    default:
+      launch_weights<AdamwWeights::kBf16Master>(g_f32, state8, form.steps, form.groups, h, items,
+                                                first, form.n, s);
   }
+  return hipGetLastError();
 }
 
 hipError_t launch_adamw_state_values(bool second, const uint8_t* codes, const uint8_t* exps,
                                      int64_t n, uint16_t* out, hipStream_t s) {
-  int64_t blocks = (n + kThreads * kVec - 1) / (kThreads * kVec);
+  int64_t blocks = (n + kThreads * kValues - 1) / (kThreads * kValues);
   if (blocks > (1 << 20)) blocks = 1 << 20;
-  const bool vec = on(codes, kVec) && on(out, 2 * kVec);
+  const bool vec = on(codes, 16) && on(out, 16);
   if (second)
     hipLaunchKernelGGL((state_values_kernel<true>), dim3((unsigned)blocks), dim3(kThreads), 0, s,
                        codes, exps, n, vec, out);

@@ -73,6 +73,8 @@ struct AdamwItem {
   int64_t n;
   float weight_decay;
   uint32_t dither0;   // counter of the tensor's first entry
+  int32_t vec;        // every array on a boundary of whole vectors
+  int32_t pad;
 };
 struct AdamwScalars {
   float lr, b1, b2, c1, c2, eps;   // c = 1 - beta
@@ -80,10 +82,26 @@ struct AdamwScalars {
   uint32_t dither_step;
   const float* grad_scale;
 };
-// Tensors of one variant (weight form, gradient type, state form) in order.
 enum class AdamwWeights { kF32, kBf16, kBf16Master };
-hipError_t launch_adamw(AdamwWeights weights, bool g_f32, bool state8, const AdamwItem* const* items,
-                        int n, const AdamwScalars& h, hipStream_t s);
+// The tensors of one form (weights, gradient type, state type) in a table: n
+// items and their first work-groups, of `steps` steps each.
+struct AdamwForm {
+  int32_t n, groups, steps;
+  uint32_t off_items, off_first;   // bytes from the table's start
+};
+constexpr int kAdamwForms = 12;
+struct AdamwTable {
+  uint64_t magic;
+  uint64_t bytes;
+  AdamwForm form[kAdamwForms];   // weights * 4 + fp32 gradient * 2 + 8-bit states
+};
+// Fills in a form's steps, groups, first work-groups and the items' vec (n and
+// the items are set); false where the work-groups do not fit a launch.
+bool adamw_lay_out(AdamwForm* form, AdamwItem* items, int32_t* first, bool g_f32, bool state8,
+                   AdamwWeights weights);
+hipError_t launch_adamw(AdamwWeights weights, bool g_f32, bool state8, const AdamwForm& form,
+                        const AdamwItem* items, const int32_t* first, const AdamwScalars& h,
+                        hipStream_t s);
 hipError_t launch_adamw_state_values(bool second, const uint8_t* codes, const uint8_t* exps,
                                      int64_t n, uint16_t* out, hipStream_t s);
 

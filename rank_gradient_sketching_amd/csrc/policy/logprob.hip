@@ -99,17 +99,18 @@ __device__ __forceinline__ State wave_state(State st, float l2t) {
 // Adds G elements; mc = st.m l2t goes along.
 template <int G>
 __device__ __forceinline__ void add_group(State& st, float& mc, const float* z, float l2t) {
-  float gs = 0.0f, gu = 0.0f;
+  float gs, gu;
 #pragma unroll
   for (int e = 0; e < G; ++e) {
     const float d = fmaf(z[e], l2t, -mc);
     const float w = exp2_normal(d);
-    gs += w;
-    gu = fmaf(w, d, gu);
+    gs = e ? gs + w : w;
+    gu = e ? fmaf(w, d, gu) : w * d;
   }
   // (2^10: the reference stays near enough for H to lose no more than ln 2^10
   // roundings where ln s and u / s nearly cancel)
-  if (__builtin_expect(!(gs <= 0x1p10f) || gu != gu, 0)) {
+  const bool careful = !(gs <= 0x1p10f) || gu != gu;
+  if (__builtin_expect(__ballot(careful) != 0, 0) && careful) {
     float gmax = z[0];
 #pragma unroll
     for (int e = 1; e < G; ++e) gmax = fmaxf(gmax, z[e]);
@@ -330,9 +331,11 @@ __device__ __forceinline__ void best_tokens(BestKeys& b, const T* z, int V, int 
 }
 
 // ---------------------------------------------------------------- loads
-// Eight elements of a lane: a wave covers 512 consecutive columns from `col`
-// (the wave's first) with whole 16-byte loads.  bf16: one load, columns col + 8
-// lane + e.  fp32: two, columns col + 4 lane + e and 256 further.
+// Eight elements of a lane: a wave covers 512 consecutive columns from `col` (the
+// same in all of its lanes) with whole 16-byte loads.  bf16: one load, columns col
+// + 8 lane + e.  fp32: two, columns col + 4 lane + e and 256 further.  load and
+// store take the address of column col and a whole group; the tail forms take the
+// row and stop at `end` (elements past it are -inf).
 template <class T>
 struct Group;
 template <>
@@ -345,43 +348,26 @@ struct Group<uint16_t> {
   static __device__ __forceinline__ int64_t column(int64_t col, int e) {
     return col + 8 * (int)(threadIdx.x & 63) + e;
   }
-  // The elements where the group is whole (zeros else), for values(), which reads
-  // a group cut off at `end` one by one; columns past it are -inf.
-  static __device__ __forceinline__ Raw fetch(const uint16_t* row, int64_t col, int64_t end) {
-    const int64_t at = column(col, 0);
-    if (at + 8 > end) return Raw{u32x4{0, 0, 0, 0}};
-    return Raw{__builtin_nontemporal_load(reinterpret_cast<const u32x4*>(row + at))};
+  static __device__ __forceinline__ Raw load(const uint16_t* at) {
+    return Raw{__builtin_nontemporal_load(reinterpret_cast<const u32x4*>(at) + (threadIdx.x & 63))};
   }
-  static __device__ __forceinline__ void values(const Raw& r, const uint16_t* row, int64_t col,
-                                                int64_t end, float* z) {
+  static __device__ __forceinline__ void values(const Raw& r, float* z) {
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
       z[2 * p] = bf16_lo(r.v[p]);
       z[2 * p + 1] = bf16_hi(r.v[p]);
     }
-    const int64_t at = column(col, 0);
-    if (at + 8 > end) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = at + e < end ? bf16_to_f32(row[at + e]) : -INFINITY;
-    }
   }
-  static __device__ __forceinline__ void store(uint16_t* row, int64_t col, int64_t end,
-                                               const float* z) {
-    const int64_t at = column(col, 0);
-    if (at + 8 <= end) {
-      u32x4 v;
+  static __device__ __forceinline__ void store(uint16_t* at, const float* z) {
+    u32x4 v;
 #pragma unroll
-      for (int p = 0; p < 4; ++p) v[p] = pack_bf16x2(z[2 * p], z[2 * p + 1]);
-      __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(row + at));
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (at + e < end) row[at + e] = f32_to_bf16(z[e]);
-    }
+    for (int p = 0; p < 4; ++p) v[p] = pack_bf16x2(z[2 * p], z[2 * p + 1]);
+    __builtin_nontemporal_store(v, reinterpret_cast<u32x4*>(at) + (threadIdx.x & 63));
   }
   static __device__ __forceinline__ float one(const uint16_t* row, int64_t col) {
     return bf16_to_f32(row[col]);
   }
+  static __device__ __forceinline__ uint16_t of(float x) { return f32_to_bf16(x); }
 };
 template <>
 struct Group<float> {
@@ -393,47 +379,46 @@ struct Group<float> {
   static __device__ __forceinline__ int64_t column(int64_t col, int e) {
     return col + 4 * (int)(threadIdx.x & 63) + (e & 3) + 256 * (e >> 2);
   }
-  static __device__ __forceinline__ Raw fetch(const float* row, int64_t col, int64_t end) {
+  static __device__ __forceinline__ Raw load(const float* at) {
     Raw r;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t at = column(col, 4 * i);
-      r.v[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      if (at + 4 <= end)
-        r.v[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(row + at));
-    }
+    for (int i = 0; i < 2; ++i)
+      r.v[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(at) + 64 * i +
+                                          (threadIdx.x & 63));
     return r;
   }
-  static __device__ __forceinline__ void values(const Raw& r, const float* row, int64_t col,
-                                                int64_t end, float* z) {
+  static __device__ __forceinline__ void values(const Raw& r, float* z) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int64_t at = column(col, 4 * i);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) z[4 * i + e] = r.v[i][e];
-      if (at + 4 > end) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) z[4 * i + e] = at + e < end ? row[at + e] : -INFINITY;
-      }
-    }
+    for (int e = 0; e < 8; ++e) z[e] = r.v[e >> 2][e & 3];
   }
-  static __device__ __forceinline__ void store(float* row, int64_t col, int64_t end,
-                                               const float* z) {
+  static __device__ __forceinline__ void store(float* at, const float* z) {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int64_t at = column(col, 4 * i);
-      if (at + 4 <= end) {
-        const f32x4 v = {z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]};
-        __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(row + at));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (at + e < end) row[at + e] = z[4 * i + e];
-      }
+      const f32x4 v = {z[4 * i], z[4 * i + 1], z[4 * i + 2], z[4 * i + 3]};
+      __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(at) + 64 * i + (threadIdx.x & 63));
     }
   }
   static __device__ __forceinline__ float one(const float* row, int64_t col) { return row[col]; }
+  static __device__ __forceinline__ float of(float x) { return x; }
 };
+template <class T>
+__device__ __forceinline__ void load_tail(const T* row, int64_t col, int64_t end, float* z) {
+  typedef Group<T> GT;
+#pragma unroll
+  for (int e = 0; e < GT::G; ++e) {
+    const int64_t at = GT::column(col, e);
+    z[e] = at < end ? GT::one(row, at) : -INFINITY;
+  }
+}
+template <class T>
+__device__ __forceinline__ void store_tail(T* row, int64_t col, int64_t end, const float* z) {
+  typedef Group<T> GT;
+#pragma unroll
+  for (int e = 0; e < GT::G; ++e) {
+    const int64_t at = GT::column(col, e);
+    if (at < end) row[at] = GT::of(z[e]);
+  }
+}
 
 constexpr int kWaveCols = 512;                    // columns of a wave's group
 constexpr int64_t kStepCols = kWaves * kWaveCols;  // of a work-group's
@@ -500,7 +485,7 @@ __global__ __launch_bounds__(kThreads) void logprob_rows_kernel(LogprobArgs a, i
   __shared__ State wst[kWaves];
   __shared__ int waiting[kWaves];
   __shared__ u64 wbuf[TOP ? kWaves * kBuf : 1];
-  const int wave = threadIdx.x >> 6;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63;
   const float l2t = kLog2e / a.tau;
   const int64_t n_tasks = a.n_tok * n_split;
@@ -518,28 +503,44 @@ __global__ __launch_bounds__(kThreads) void logprob_rows_kernel(LogprobArgs a, i
     float mc = st.m * l2t;
     BestKeys bk = no_keys(wbuf + (TOP ? wave * kBuf : 0));
     bool first = true;
-    // Whole waves stay in the loop (a wave's first column decides); kDeep groups
-    // are loaded ahead of their use.
+    auto add = [&](const float* v, int64_t c) {
+      add_group<GT::G>(st, mc, v, l2t);
+      if constexpr (TOP) {
+        offer_group<GT>(bk, v, c, first, a.n_top);
+        first = false;
+      }
+    };
+    // This wave's groups: whole ones, kDeep loaded ahead of their use (past the
+    // last one it is loaded again, which spares the loop a condition), then what
+    // is left of the piece.
     constexpr int kDeep = 2;
-    const int64_t wc = c0 + wave * kWaveCols;
-    typename GT::Raw raw[kDeep];
-#pragma unroll
-    for (int i = 0; i < kDeep; ++i)
-      if (wc + i * kStepCols < c1) raw[i] = GT::fetch(z, wc + i * kStepCols, c1);
-    for (int64_t cc = wc; cc < c1; cc += kDeep * kStepCols) {
+    int64_t c = c0 + wave * kWaveCols;
+    const int64_t whole = c + kWaveCols <= c1 ? (c1 - kWaveCols - c) / kStepCols + 1 : 0;
+    if (whole > 0) {
+      const int64_t last = c + (whole - 1) * kStepCols;
+      typename GT::Raw raw[kDeep];
 #pragma unroll
       for (int i = 0; i < kDeep; ++i) {
-        const int64_t c = cc + i * kStepCols;
-        if (c >= c1) break;
-        float v[GT::G];
-        GT::values(raw[i], z, c, c1, v);
-        if (c + kDeep * kStepCols < c1) raw[i] = GT::fetch(z, c + kDeep * kStepCols, c1);
-        add_group<GT::G>(st, mc, v, l2t);
-        if constexpr (TOP) {
-          offer_group<GT>(bk, v, c, first, a.n_top);
-          first = false;
+        const int64_t at = c + i * kStepCols;
+        raw[i] = GT::load(z + (at < last ? at : last));
+      }
+      while (c <= last) {
+#pragma unroll
+        for (int i = 0; i < kDeep; ++i) {
+          if (c > last) break;
+          float v[GT::G];
+          GT::values(raw[i], v);
+          const int64_t at = c + kDeep * kStepCols;
+          raw[i] = GT::load(z + (at < last ? at : last));
+          add(v, c);
+          c += kStepCols;
         }
       }
+    }
+    if (c < c1) {
+      float v[GT::G];
+      load_tail(z, c, c1, v);
+      add(v, c);
     }
     st = wave_state(st, l2t);
     if (lane == 0) {
@@ -637,31 +638,31 @@ __global__ __launch_bounds__(64) void logprob_join_kernel(LogprobArgs a, int n_s
   }
 }
 
-// dz over pieces of kGradGroups groups per thread.
-constexpr int kGradGroups = 4;
-constexpr int64_t kGradCols = kStepCols * kGradGroups;
+// dz over pieces of grad_groups groups per thread: 64 bytes of logits in flight
+// per lane (4096 x 152064 bf16: 2, 4, 8 groups 417, 400, 428 us; 501 x 32003 fp32:
+// 2, 4, 8 groups 23.0, 25.0, 28.2 us).
+constexpr int grad_groups(size_t elem) { return elem == 2 ? 4 : 2; }
+constexpr int64_t grad_cols(size_t elem) { return kStepCols * grad_groups(elem); }
 
 template <class T>
 __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs a, int n_pieces) {
   typedef Group<T> GT;
   constexpr int G = GT::G;
+  constexpr int kGradGroups = grad_groups(sizeof(T));
   const int64_t n_tasks = a.n_tok * n_pieces;
   const int64_t V = a.vocab;
-  // 1 / tau as two floats: z / tau keeps fp32 accuracy in one fused step
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // 1 / tau as two floats: z / tau keeps fp32 accuracy in one fused step (a bf16
+  // result has no use for it)
   const float ih = 1.0f / a.tau;
   const float il = fmaf(-a.tau, ih, 1.0f) / a.tau;
   for (int64_t task = blockIdx.x; task < n_tasks; task += gridDim.x) {
     const int64_t row = task / n_pieces;
-    const int64_t c0 = (task - row * n_pieces) * kGradCols + (threadIdx.x >> 6) * kWaveCols;
+    const int64_t c0 = (task - row * n_pieces) * grad_cols(sizeof(T)) + wave * kWaveCols;
     const T* z = static_cast<const T*>(a.z) + row * a.ld;
     T* dz = static_cast<T*>(a.dz) + row * a.ldz;
     const int64_t target = a.target ? a.target[row] : -1;
-    if (a.target && (target < 0 || target >= V)) {
-      const float zero[G] = {};
-#pragma unroll
-      for (int i = 0; i < kGradGroups; ++i) GT::store(dz, c0 + i * kStepCols, V, zero);
-      continue;
-    }
+    const bool out = a.target && (target < 0 || target >= V);
     const float lse = a.lse[row];
     const float g = a.d_logp ? a.d_logp[row] : 0.0f;
     const float gl = a.d_lse ? a.d_lse[row] : 0.0f;
@@ -669,24 +670,54 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
     const float H = a.d_entropy ? a.entropy[row] : 0.0f;
     // dz_j = p_j (k0 + k1 log p_j) + [j = target] kt
     const float k0 = (gl - g - gh * H) * ih, k1 = -gh * ih, kt = g * ih;
-    typename GT::Raw raw[kGradGroups];
-#pragma unroll
-    for (int i = 0; i < kGradGroups; ++i) raw[i] = GT::fetch(z, c0 + i * kStepCols, V);
-#pragma unroll
-    for (int i = 0; i < kGradGroups; ++i) {
-      const int64_t c = c0 + i * kStepCols;
-      float v[G];
-      GT::values(raw[i], z, c, V, v);
+    auto gradient = [&](float* v, int64_t c) {
 #pragma unroll
       for (int e = 0; e < G; ++e) {
-        const float lp = fmaf(v[e], ih, fmaf(v[e] == -INFINITY ? 0.0f : v[e], il, -lse));
+        // (a masked token: p = 0, and log p kept finite)
+        const float low = sizeof(T) == 4 ? fmaf(fmaxf(v[e], kMinFloat), il, -lse) : -lse;
+        const float lp = fmaf(v[e], ih, low);
         const float p = exp2_normal(lp * kLog2e);
-        // (a masked token: p = 0 and log p kept finite)
-        float o = p * fmaf(k1, fmaxf(lp, kLow), k0);
-        if (GT::column(c, e) == target) o += kt;
-        v[e] = o;
+        v[e] = p * fmaf(k1, fmaxf(lp, kLow), k0);
       }
-      GT::store(dz, c, V, v);
+      if (target >= c && target < c + kWaveCols) {
+#pragma unroll
+        for (int e = 0; e < G; ++e)
+          if (GT::column(c, e) == target) v[e] += kt;
+      }
+      if (out) {
+#pragma unroll
+        for (int e = 0; e < G; ++e) v[e] = 0.0f;
+      }
+    };
+    if (c0 + (kGradGroups - 1) * kStepCols + kWaveCols <= V) {
+      typename GT::Raw raw[kGradGroups];
+#pragma unroll
+      for (int i = 0; i < kGradGroups; ++i)
+        if (!out) raw[i] = GT::load(z + c0 + i * kStepCols);
+#pragma unroll
+      for (int i = 0; i < kGradGroups; ++i) {
+        const int64_t c = c0 + i * kStepCols;
+        float v[G];
+        GT::values(raw[i], v);
+        gradient(v, c);
+        GT::store(dz + c, v);
+      }
+    } else {
+#pragma unroll 1
+      for (int i = 0; i < kGradGroups; ++i) {
+        const int64_t c = c0 + i * kStepCols;
+        if (c >= V) break;
+        float v[G];
+        if (c + kWaveCols <= V) {
+          GT::values(GT::load(z + c), v);
+          gradient(v, c);
+          GT::store(dz + c, v);
+        } else {
+          load_tail(z, c, V, v);
+          gradient(v, c);
+          store_tail(dz, c, V, v);
+        }
+      }
     }
   }
 }
@@ -721,7 +752,7 @@ hipError_t launch_rows(const LogprobArgs& a, const LogprobPlan& p, char* ws, hip
 
 template <class T>
 hipError_t launch_grad(const LogprobGradArgs& a, hipStream_t s) {
-  const int n_pieces = (int)((a.vocab + kGradCols - 1) / kGradCols);
+  const int n_pieces = (int)((a.vocab + grad_cols(sizeof(T)) - 1) / grad_cols(sizeof(T)));
   const int64_t tasks = a.n_tok * n_pieces;
   hipLaunchKernelGGL((logprob_grad_kernel<T>), dim3((unsigned)(tasks < kMaxGrid ? tasks : kMaxGrid)),
                      dim3(kThreads), 0, s, a, n_pieces);

@@ -7,8 +7,8 @@ Argument marshalling only, as in api.py: the work runs in the library's HIP
 kernels on the tensors' device, asynchronously on torch's current stream of
 that device.  Tensors must live on the GPU; nothing here falls back to the CPU.
 """
-import contextlib
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -18,33 +18,48 @@ from .api import _rows, _stream, _ws
 
 MAX_TOP = 64         # LOGRA_MAX_TOP
 STATE_BLOCK = 32     # LOGRA_STATE_BLOCK
+_BF16 = (torch.bfloat16,)
+_F32 = (torch.float32,)
+_EITHER = (torch.bfloat16, torch.float32)
+_I32, _I64, _U8 = (torch.int32,), (torch.int64,), (torch.uint8,)
 _TYPES = {torch.bfloat16: 0, torch.float32: 1}   # LOGRA_BF16, LOGRA_F32
-_same_device = contextlib.nullcontext()
+# (the raw lookup spares torch.cuda.current_device's initialisation check: every
+# tensor that gets here is on the GPU already)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _need(t, name, dtypes, device=None, shape=None, ndim=None, contiguous=False):
-    """Checks one tensor argument; dtypes: the types it may have."""
+def _need(t, name, dtypes, dev=None, shape=None, ndim=None, contiguous=False):
+    """Checks one tensor argument: dtypes it may have, device index, shape."""
+    if (isinstance(t, torch.Tensor) and t.is_cuda and t.dtype in dtypes
+            and (dev is None or t.get_device() == dev) and (ndim is None or t.dim() == ndim)
+            and (shape is None or t.shape == shape) and (not contiguous or t.is_contiguous())):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor (got {t.device})")
-    if device is not None and t.device != device:
-        raise ValueError(f"{name} must be on {device} (got {t.device})")
     if t.dtype not in dtypes:
-        want = " or ".join(str(d) for d in dtypes)
-        raise ValueError(f"{name} must be {want} (got {t.dtype})")
+        raise ValueError(f"{name} must be {' or '.join(map(str, dtypes))} (got {t.dtype})")
+    if dev is not None and t.get_device() != dev:
+        raise ValueError(f"{name} must be on GPU {dev} (got {t.device})")
     if ndim is not None and t.dim() != ndim:
         raise ValueError(f"{name} must have {ndim} dims (got {t.dim()})")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _on(device):
-    """Launches go to the current device, so make it the tensors' own."""
-    return (_same_device if device.index == torch.cuda.current_device()
-            else torch.cuda.device(device))
+def _call(name, dev, *args):
+    """One library call; launches go to the current device, so the tensors' own
+    is made current."""
+    fn = getattr(_lib.lib(), name)
+    if dev == _current_device():
+        st = fn(*args)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args)
+    if st != 0:
+        _lib.check(st, name)
 
 
 def _matrix(t, name):
@@ -54,22 +69,25 @@ def _matrix(t, name):
     return rows, cols, ld if rows > 1 else -(-cols // 8) * 8
 
 
-def _opt(t, name, n, device, dtype=torch.float32):
+def _opt(t, name, n, dev, dtypes=_F32):
     """Address of an optional vector of n entries."""
     if t is None:
         return None
-    _need(t, name, (dtype,), device, shape=(n,), contiguous=True)
+    _need(t, name, dtypes, dev, (n,), contiguous=True)
     return t.data_ptr()
 
 
-def _workspace(ws, need, device):
+def _workspace(ws, need, like):
+    """(address, bytes, tensor) of scratch for a call; the tensor is held until
+    the call is enqueued."""
     if need == 0:
-        return None, 0
+        return None, 0, None
     if ws is None:
-        ws = torch.empty(need, dtype=torch.uint8, device=device)
-    elif isinstance(ws, torch.Tensor) and ws.device != device:
-        raise ValueError(f"ws must be on {device} (got {ws.device})")
-    return _ws(ws)
+        ws = torch.empty(need, dtype=torch.uint8, device=like.device)
+        return ws.data_ptr(), need, ws
+    if isinstance(ws, torch.Tensor) and ws.is_cuda and ws.get_device() != like.get_device():
+        raise ValueError(f"ws must be on {like.device} (got {ws.device})")
+    return (*_ws(ws), ws)
 
 
 # ------------------------------------------------------------------ log probabilities
@@ -83,6 +101,7 @@ class TokenLogprob(NamedTuple):
     top_logp: Optional[torch.Tensor]
 
 
+@functools.lru_cache(maxsize=256)
 def token_logprob_ws_bytes(n_tok, vocab, n_top=0):
     return int(_lib.lib().logra_token_logprob_ws_bytes(n_tok, vocab, n_top))
 
@@ -99,33 +118,37 @@ def token_logprob(z, target=None, tau=1.0, n_top=0, out=None, ws=None):
     out: a TokenLogprob of contiguous tensors to write; its None entries are
     not computed (top_* are given exactly when n_top > 0).  ws: scratch of
     token_logprob_ws_bytes(n, vocab, n_top) bytes."""
-    _need(z, "z", (torch.bfloat16, torch.float32), ndim=2)
+    _need(z, "z", _EITHER, ndim=2)
     n, V, ld = _matrix(z, "z")
-    dev = z.device
+    dev = z.get_device()
     n_top = int(n_top)
     if not 0 <= n_top <= MAX_TOP:
         raise ValueError(f"n_top must be between 0 and {MAX_TOP}")
     if out is None:
-        rows = torch.empty((2 if target is None else 3, n), dtype=torch.float32, device=dev)
-        top = ((torch.empty((n, n_top), dtype=torch.int32, device=dev),
-                torch.empty((n, n_top), dtype=torch.float32, device=dev))
-               if n_top else (None, None))
-        out = TokenLogprob(None if target is None else rows[2], rows[0], rows[1], *top)
-    if (out.top_idx is None) != (n_top == 0) or (out.top_logp is None) != (n_top == 0):
-        raise ValueError("out.top_idx and out.top_logp go with n_top > 0")
-    if n_top:
-        _need(out.top_idx, "out.top_idx", (torch.int32,), dev, (n, n_top), contiguous=True)
-        _need(out.top_logp, "out.top_logp", (torch.float32,), dev, (n, n_top), contiguous=True)
-    if out.logp is not None and target is None:
-        raise ValueError("logp needs target")
-    ptrs = [_opt(getattr(out, x), f"out.{x}", n, dev) for x in ("logp", "entropy", "lse")]
-    ptrs += [t.data_ptr() if n_top else None for t in (out.top_idx, out.top_logp)]
-    t_ptr = _opt(target, "target", n, dev, torch.int64)
-    ws_ptr, ws_n = _workspace(ws, token_logprob_ws_bytes(n, V, n_top), dev)
-    with _on(dev):
-        st = _lib.lib().logra_token_logprob(z.data_ptr(), _TYPES[z.dtype], n, V, ld, t_ptr,
-                                            float(tau), n_top, *ptrs, ws_ptr, ws_n, _stream(z))
-    _lib.check(st, "logra_token_logprob")
+        rows = torch.empty((2 if target is None else 3, n), dtype=torch.float32,
+                           device=z.device).unbind(0)
+        idx = top = None
+        if n_top:
+            idx = torch.empty((n, n_top), dtype=torch.int32, device=z.device)
+            top = torch.empty((n, n_top), dtype=torch.float32, device=z.device)
+        out = TokenLogprob(None if target is None else rows[2], rows[0], rows[1], idx, top)
+        ptrs = [None if t is None else t.data_ptr() for t in out]
+    else:
+        if (out.top_idx is None) != (n_top == 0) or (out.top_logp is None) != (n_top == 0):
+            raise ValueError("out.top_idx and out.top_logp go with n_top > 0")
+        if out.logp is not None and target is None:
+            raise ValueError("logp needs target")
+        ptrs = [_opt(getattr(out, x), f"out.{x}", n, dev) for x in ("logp", "entropy", "lse")]
+        if n_top:
+            _need(out.top_idx, "out.top_idx", _I32, dev, (n, n_top), contiguous=True)
+            _need(out.top_logp, "out.top_logp", _F32, dev, (n, n_top), contiguous=True)
+            ptrs += [out.top_idx.data_ptr(), out.top_logp.data_ptr()]
+        else:
+            ptrs += [None, None]
+    t_ptr = _opt(target, "target", n, dev, _I64)
+    ws_ptr, ws_n, ws = _workspace(ws, token_logprob_ws_bytes(n, V, n_top), z)
+    _call("logra_token_logprob", dev, z.data_ptr(), _TYPES[z.dtype], n, V, ld, t_ptr, tau, n_top,
+          *ptrs, ws_ptr, ws_n, _stream(z))
     return out
 
 
@@ -137,24 +160,25 @@ def token_logprob_backward(z, target, lse, entropy=None, d_logp=None, d_entropy=
     d_lse p_j) / tau.  lse (and entropy, with d_entropy) are those of
     token_logprob for the same z and tau.  Rows left out get zeros.  dz: a
     tensor like z to write (z itself: the gradient replaces the logits)."""
-    _need(z, "z", (torch.bfloat16, torch.float32), ndim=2)
+    _need(z, "z", _EITHER, ndim=2)
     n, V, ld = _matrix(z, "z")
-    dev = z.device
+    dev = z.get_device()
     if dz is None:
         pad = 16 // z.element_size()
-        dz = torch.empty((n, -(-V // pad) * pad), dtype=z.dtype, device=dev)[:, :V]
-    _need(dz, "dz", (z.dtype,), dev, (n, V))
-    ldz = _matrix(dz, "dz")[2]
-    _need(lse, "lse", (torch.float32,), dev, (n,), contiguous=True)
-    ptrs = [_opt(t, name, n, dev) for name, t in
-            (("entropy", entropy), ("d_logp", d_logp), ("d_entropy", d_entropy),
-             ("d_lse", d_lse))]
-    t_ptr = _opt(target, "target", n, dev, torch.int64)
-    with _on(dev):
-        st = _lib.lib().logra_token_logprob_backward(
-            z.data_ptr(), _TYPES[z.dtype], n, V, ld, t_ptr, float(tau), lse.data_ptr(), *ptrs,
-            dz.data_ptr(), ldz, _stream(z))
-    _lib.check(st, "logra_token_logprob_backward")
+        cols = -(-V // pad) * pad
+        dz = torch.empty((n, cols), dtype=z.dtype, device=z.device)
+        ldz = cols if n > 1 else -(-V // 8) * 8
+        if cols != V:
+            dz = dz[:, :V]
+    else:
+        _need(dz, "dz", (z.dtype,), dev, (n, V))
+        ldz = _matrix(dz, "dz")[2]
+    _need(lse, "lse", _F32, dev, (n,), contiguous=True)
+    _call("logra_token_logprob_backward", dev, z.data_ptr(), _TYPES[z.dtype], n, V, ld,
+          _opt(target, "target", n, dev, _I64), tau, lse.data_ptr(),
+          _opt(entropy, "entropy", n, dev), _opt(d_logp, "d_logp", n, dev),
+          _opt(d_entropy, "d_entropy", n, dev), _opt(d_lse, "d_lse", n, dev), dz.data_ptr(), ldz,
+          _stream(z))
     return dz
 
 
@@ -162,34 +186,32 @@ def token_logprob_backward(z, target, lse, entropy=None, d_logp=None, d_entropy=
 class _Bound:
     """Tensors of an AdamW step, checked and laid out once (adamw_bind)."""
 
-    def __init__(self, items, device, keep):
-        self.items, self.device = items, device
-        self._keep = keep      # the bound storage lives as long as the addresses
+    def __init__(self, n, table, table_dev, keep):
+        self.n, self.table, self.table_dev = n, table, table_dev
+        self.device = table_dev.device
+        self.address = ctypes.addressof(table)
+        self._keep = keep      # the bound storage lives as long as its addresses
 
     def __len__(self):
-        return len(self.items)
+        return self.n
 
 
-def _lists(n, **named):
-    out = []
-    for name, x in named.items():
-        if x is None:
-            x = [None] * n
-        if len(x) != n:
-            raise ValueError(f"{name} must have {n} entries (got {len(x)})")
-        out.append(list(x))
-    return out
+def _listed(x, n, name):
+    x = [None] * n if x is None else list(x)
+    if len(x) != n:
+        raise ValueError(f"{name} must have {n} entries (got {len(x)})")
+    return x
 
 
 def _check_apart(spans):
     """spans: (low, high, written, name); raises where a written one overlaps."""
-    spans.sort(key=lambda x: (x[0], x[1]))
+    spans.sort(key=lambda x: x[:2])
     reach, by, w_reach, w_by = 0, None, 0, None      # the furthest of all, and of the written
     for lo, hi, written, name in spans:
         if hi <= lo:
             continue
         if lo < w_reach or (written and lo < reach):
-            raise ValueError(f"{name} overlaps {w_by if lo < w_reach else by}")
+            raise ValueError("%s[%d] overlaps %s[%d]" % (name + (w_by if lo < w_reach else by)))
         if hi > reach:
             reach, by = hi, name
         if written and hi > w_reach:
@@ -204,54 +226,62 @@ def adamw_bind(params, grads, m, v, master=None, m_exp=None, v_exp=None, weight_
     zero is the zero state), master (fp32 weights behind bf16 params, or None
     entries); weight_decay: one number or a list.  All contiguous, on one GPU.
     The handle keeps the storage that the tensors have now and steps that:
-    bind again after giving a tensor other storage (e.g. a new gradient)."""
+    bind again after giving a tensor other storage (e.g. a new gradient).  It
+    copies a table to the GPU, so it is made outside a stream capture."""
     params = list(params)
     n = len(params)
     if n == 0:
         raise ValueError("params is empty")
-    grads, m, v, master, m_exp, v_exp = _lists(n, grads=grads, m=m, v=v, master=master,
-                                               m_exp=m_exp, v_exp=v_exp)
+    columns = [("p", params, _EITHER, 1), ("g", _listed(grads, n, "grads"), _EITHER, 1),
+               ("m", _listed(m, n, "m"), _F32, 1), ("v", _listed(v, n, "v"), _F32, 1),
+               ("master", _listed(master, n, "master"), _F32, 1),
+               ("m_exp", _listed(m_exp, n, "m_exp"), _U8, STATE_BLOCK),
+               ("v_exp", _listed(v_exp, n, "v_exp"), _U8, STATE_BLOCK)]
     decay = (list(weight_decay) if isinstance(weight_decay, (list, tuple))
              else [weight_decay] * n)
     if len(decay) != n:
         raise ValueError(f"weight_decay must have {n} entries (got {len(decay)})")
     items = (_lib.AdamWItem * n)()
     keep, spans, dev = [], [], None
-    both = (torch.bfloat16, torch.float32)
+    exps = columns[5][1], columns[6][1]
     for i in range(n):
         p = params[i]
-        _need(p, f"params[{i}]", both, dev, contiguous=True)
-        dev = p.device
+        if dev is None:
+            _need(p, "p[0]", _EITHER)
+            dev = p.get_device()
         k = p.numel()
         q = items[i]
-        q.n, q.weight_decay = k, float(decay[i])
-        q.p_type, q.g_type = _TYPES[p.dtype], 0
-        state8 = m_exp[i] is not None or v_exp[i] is not None
-        st = (torch.uint8,) if state8 else (torch.float32,)
-        blocks = -(-k // STATE_BLOCK)
-        for name, t, types, size, written in (
-                ("p", p, both, k, True), ("g", grads[i], both, k, False),
-                ("m", m[i], st, k, True), ("v", v[i], st, k, True),
-                ("master", master[i], (torch.float32,), k, True),
-                ("m_exp", m_exp[i], (torch.uint8,), blocks, True),
-                ("v_exp", v_exp[i], (torch.uint8,), blocks, True)):
+        state8 = exps[0][i] is not None or exps[1][i] is not None
+        for name, column, types, block in columns:
+            t = column[i]
             if t is None:
-                if name == "master" or (name.endswith("_exp") and not state8):
+                if name == "master" or (block > 1 and not state8):
                     continue
                 raise ValueError(f"{name}[{i}] is missing")
-            _need(t, f"{name}[{i}]", types, dev, contiguous=True)
-            if t.numel() != size:
-                raise ValueError(f"{name}[{i}] must have {size} entries (got {t.numel()})")
-            if name == "g":
-                q.g_type = _TYPES[t.dtype]
-            if name == "master" and p.dtype != torch.bfloat16:
-                raise ValueError(f"master[{i}] needs a bf16 parameter")
-            setattr(q, name, t.data_ptr())
-            spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), written,
-                          f"{name}[{i}]"))
-            keep.append(t.detach())
+            if state8 and name in ("m", "v"):
+                types = _U8
+            if not (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == dev
+                    and t.dtype in types and t.is_contiguous()):
+                _need(t, f"{name}[{i}]", types, dev, contiguous=True)
+            size = t.numel()
+            if size != -(-k // block):
+                raise ValueError(f"{name}[{i}] must have {-(-k // block)} entries (got {size})")
+            at = t.data_ptr()
+            setattr(q, name, at)
+            spans.append((at, at + size * t.element_size(), name != "g", (name, i)))
+            keep.append(t)
+        if q.master is not None and p.dtype != torch.bfloat16:
+            raise ValueError(f"master[{i}] needs a bf16 parameter")
+        q.n, q.weight_decay = k, decay[i]
+        q.p_type, q.g_type = _TYPES[p.dtype], _TYPES[columns[1][1][i].dtype]
     _check_apart(spans)
-    return _Bound(items, dev, keep)
+    # (an alias each: a tensor given other storage does not free this one)
+    keep = [t.detach() for t in keep]
+    size = int(_lib.lib().logra_adamw_table_bytes(n))
+    table = (ctypes.c_uint64 * (size // 8))()
+    _lib.check(_lib.lib().logra_adamw_table(n, items, table, size), "logra_adamw_table")
+    table_dev = torch.frombuffer(table, dtype=torch.uint8).to(params[0].device)
+    return _Bound(n, table, table_dev, keep)
 
 
 def adamw_step(bound, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, grad_scale=None):
@@ -264,17 +294,15 @@ def adamw_step(bound, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, grad_scale=Non
     sketch_update steps a sketch.  Returns None."""
     if not isinstance(bound, _Bound):
         raise TypeError("bound must be a handle of adamw_bind")
+    dev = bound.table_dev.get_device()
     scale = None
     if grad_scale is not None:
-        _need(grad_scale, "grad_scale", (torch.float32,), bound.device)
+        _need(grad_scale, "grad_scale", _F32, dev)
         if grad_scale.numel() != 1:
             raise ValueError("grad_scale must have one entry")
         scale = grad_scale.data_ptr()
-    with _on(bound.device):
-        st = _lib.lib().logra_adamw_step(len(bound.items), bound.items, float(lr), float(beta1),
-                                         float(beta2), float(eps), int(step), scale,
-                                         _stream(bound))
-    _lib.check(st, "logra_adamw_step")
+    _call("logra_adamw_step", dev, bound.address, bound.table_dev.data_ptr(), lr, beta1, beta2,
+          eps, step, scale, _stream(bound))
 
 
 def adamw_state_values(codes, exps, which, out=None):
@@ -282,23 +310,23 @@ def adamw_state_values(codes, exps, which, out=None):
     (any shape, contiguous), exps uint8 with one entry per 32 codes."""
     if which not in ("m", "v"):
         raise ValueError('which must be "m" or "v"')
-    _need(codes, "codes", (torch.uint8,), contiguous=True)
+    _need(codes, "codes", _U8, contiguous=True)
     n = codes.numel()
-    _need(exps, "exps", (torch.uint8,), codes.device, contiguous=True)
+    dev = codes.get_device()
+    _need(exps, "exps", _U8, dev, contiguous=True)
     if exps.numel() != -(-n // STATE_BLOCK):
         raise ValueError(f"exps must have {-(-n // STATE_BLOCK)} entries (got {exps.numel()})")
     if out is None:
         out = torch.empty(codes.shape, dtype=torch.bfloat16, device=codes.device)
-    _need(out, "out", (torch.bfloat16,), codes.device, codes.shape, contiguous=True)
-    with _on(codes.device):
-        st = _lib.lib().logra_adamw_state_values(0 if which == "m" else 1, codes.data_ptr(),
-                                                 exps.data_ptr(), n, out.data_ptr(),
-                                                 _stream(codes))
-    _lib.check(st, "logra_adamw_state_values")
+    else:
+        _need(out, "out", _BF16, dev, codes.shape, contiguous=True)
+    _call("logra_adamw_state_values", dev, 0 if which == "m" else 1, codes.data_ptr(),
+          exps.data_ptr(), n, out.data_ptr(), _stream(codes))
     return out
 
 
 # ------------------------------------------------------------------ unmerged updates
+@functools.lru_cache(maxsize=256)
 def adapter_ws_bytes(T, d, k, r):
     return int(_lib.lib().logra_adapter_ws_bytes(T, d, k, r))
 
@@ -314,42 +342,41 @@ def adapter_apply(X, Y, adapter, U, scale, seeds=None, A=None, out=None, ws=None
     int64 [n, 2] (seed and stream of each policy's sign basis; c = 1/sqrt(r)),
     or A [n, r, k] bf16 (c = 1), e.g. Gaussian ones from regen_A.  ws: scratch
     of adapter_ws_bytes(T, d, k, r) bytes."""
-    _need(X, "X", (torch.bfloat16,), ndim=2)
-    dev = X.device
+    _need(X, "X", _BF16, ndim=2)
+    dev = X.get_device()
     T, k, ldx = _matrix(X, "X")
-    _need(Y, "Y", (torch.bfloat16,), dev, ndim=2)
+    _need(Y, "Y", _BF16, dev, ndim=2)
     T2, d, ldy = _matrix(Y, "Y")
     if T2 != T:
         raise ValueError(f"X has {T} rows but Y has {T2}")
     if out is None:
-        out = Y
-    _need(out, "out", (torch.bfloat16,), dev, (T, d))
-    ldo = _matrix(out, "out")[2]
-    _need(U, "U", (torch.float32, torch.bfloat16), dev, ndim=3, contiguous=True)
+        out, ldo = Y, ldy
+    else:
+        _need(out, "out", _BF16, dev, (T, d))
+        ldo = _matrix(out, "out")[2]
+    _need(U, "U", _EITHER, dev, ndim=3, contiguous=True)
     n, d2, r = U.shape
     if d2 != d:
         raise ValueError(f"Y has {d} columns but U is for {d2}")
-    _need(adapter, "adapter", (torch.int32,), dev, (T,), contiguous=True)
-    _need(scale, "scale", (torch.float32,), dev, (n,), contiguous=True)
+    _need(adapter, "adapter", _I32, dev, (T,), contiguous=True)
+    _need(scale, "scale", _F32, dev, (n,), contiguous=True)
     if (seeds is None) == (A is None):
         raise ValueError("give seeds (sign bases) or A")
     s_ptr = a_ptr = None
     lda = 0
     if seeds is not None:
-        _need(seeds, "seeds", (torch.int64,), dev, (n, 2), contiguous=True)
+        _need(seeds, "seeds", _I64, dev, (n, 2), contiguous=True)
         s_ptr = seeds.data_ptr()
     else:
-        _need(A, "A", (torch.bfloat16,), dev, (n, r, k))
-        rows = A.as_strided((n * r, k), (A.stride(1) if r > 1 else A.stride(0), A.stride(2)))
+        _need(A, "A", _BF16, dev, (n, r, k))
+        if k > 1 and A.stride(2) != 1:
+            raise ValueError("A must have contiguous rows")
         if n > 1 and r > 1 and A.stride(0) != r * A.stride(1):
             raise ValueError("the policies of A must lie r rows apart")
-        lda = _matrix(rows, "A")[2]
+        lda = A.stride(1) if r > 1 else A.stride(0) if n > 1 else -(-k // 8) * 8
         a_ptr = A.data_ptr()
-    ws_ptr, ws_n = _workspace(ws, adapter_ws_bytes(T, d, k, r), dev)
-    with _on(dev):
-        st = _lib.lib().logra_adapter_apply(
-            X.data_ptr(), ldx, Y.data_ptr(), ldy, out.data_ptr(), ldo, T, d, k, r, n,
-            adapter.data_ptr(), U.data_ptr(), _TYPES[U.dtype], s_ptr, a_ptr, lda,
-            scale.data_ptr(), ws_ptr, ws_n, _stream(X))
-    _lib.check(st, "logra_adapter_apply")
+    ws_ptr, ws_n, ws = _workspace(ws, adapter_ws_bytes(T, d, k, r), X)
+    _call("logra_adapter_apply", dev, X.data_ptr(), ldx, Y.data_ptr(), ldy, out.data_ptr(), ldo, T,
+          d, k, r, n, adapter.data_ptr(), U.data_ptr(), _TYPES[U.dtype], s_ptr, a_ptr, lda,
+          scale.data_ptr(), ws_ptr, ws_n, _stream(X))
     return out

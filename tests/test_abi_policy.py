@@ -23,7 +23,7 @@ def L():
 
 def test_exports_every_declared_symbol(L):
     declared = _lib.header_symbols(_lib.POLICY_HEADER_PATH)
-    assert len(declared) == 7
+    assert len(declared) == 9
     out = subprocess.run(["nm", "-D", "--defined-only", _lib.LIB_PATH], capture_output=True,
                          text=True, check=True).stdout
     exported = {line.split()[-1] for line in out.splitlines() if line.strip()}
@@ -98,43 +98,79 @@ def test_logprob_grad_empty(L):
 
 
 # ------------------------------------------------------------------ AdamW
-def _adamw(L, n=1, lr=1e-3, b1=0.9, b2=0.999, eps=1e-8, step=1, scale=None, items=1, **kw):
+def _table(L, n=1, items=1, table=True, short=0, **kw):
     arr = (_lib.AdamWItem * max(1, n))()
     for q in arr:
-        q.p, q.g, q.m, q.v, q.n, q.p_type, q.g_type = A, B, C, D, 0, 1, 1
+        q.p, q.g, q.m, q.v, q.n, q.p_type, q.g_type = A, B, C, D, 100, 1, 1
         for k, v in kw.items():
             setattr(q, k, v)
-    return L.logra_adamw_step(n, arr if items else None, lr, b1, b2, eps, step, scale, None)
+    size = max(L.logra_adamw_table_bytes(n), 256)
+    buf = (ctypes.c_uint64 * (size // 8))()
+    st = L.logra_adamw_table(n, arr if items else None, buf if table else None, size - short)
+    return st, buf
 
 
-@pytest.mark.parametrize("kw", [
-    dict(n=-1), dict(items=0), dict(lr=-1.0), dict(lr=NAN), dict(lr=INF), dict(b1=1.0),
-    dict(b1=-0.1), dict(b2=1.0), dict(b2=NAN), dict(b2=1.0 - 1e-12), dict(eps=-1e-8),
-    dict(eps=INF), dict(step=0), dict(scale=E + 2), dict(p_type=2), dict(g_type=-1),
-    dict(weight_decay=NAN), dict(m_exp=E), dict(v_exp=E), dict(master=W),
+@pytest.mark.parametrize("kw,status", [
+    (dict(n=-1), EINVAL), (dict(items=0), EINVAL), (dict(table=False), EINVAL),
+    (dict(short=256), EWS), (dict(p_type=2), EINVAL), (dict(g_type=-1), EINVAL),
+    (dict(weight_decay=NAN), EINVAL), (dict(m_exp=E), EINVAL), (dict(v_exp=E), EINVAL),
+    (dict(master=W), EINVAL), (dict(p=None), EINVAL), (dict(g=None), EINVAL),
+    (dict(m=None), EINVAL), (dict(v=None), EINVAL), (dict(p=A + 2), EINVAL),
+    (dict(g=B + 2), EINVAL), (dict(m=C + 1), EINVAL), (dict(v=D + 2), EINVAL),
+    (dict(p_type=0, p=A + 1), EINVAL), (dict(p_type=0, master=W + 2), EINVAL),
+    (dict(n=2, p_type=0, m_exp=E, v_exp=W, m=C + 1, v=D + 3), OK),
+    (dict(p_type=0, p=A + 2, g=B + 4), OK),
+    # sizes, also past what one launch can take
+    (dict(**{"n": 1}, weight_decay=0.1), OK),
 ])
-def test_adamw_rejects(L, kw):
-    assert _adamw(L, **kw) == EINVAL
+def test_adamw_table_rejects(L, kw, status):
+    assert _table(L, **kw)[0] == status
 
 
-@pytest.mark.parametrize("kw", [
-    dict(p=None), dict(g=None), dict(m=None), dict(v=None), dict(p=A + 2), dict(g=B + 2),
-    dict(m=C + 1), dict(v=D + 2), dict(p_type=0, p=A + 1), dict(p_type=0, master=W + 2),
-])
-def test_adamw_rejects_arrays(L, kw):
+def test_adamw_table_sizes(L):
+    assert L.logra_adamw_table_bytes(-1) == 0 and L.logra_adamw_table_bytes(1 << 25) == 0
+    assert L.logra_adamw_table_bytes(0) > 0
+    assert L.logra_adamw_table_bytes(1000) >= 1000 * 84
     arr = (_lib.AdamWItem * 1)()
     q = arr[0]
-    q.p, q.g, q.m, q.v, q.n, q.p_type, q.g_type = A, B, C, D, 100, 1, 1
-    for k, v in kw.items():
-        setattr(q, k, v)
-    assert L.logra_adamw_step(1, arr, 1e-3, 0.9, 0.999, 1e-8, 1, None, None) == EINVAL
-    q.n = -1
-    assert L.logra_adamw_step(1, arr, 1e-3, 0.9, 0.999, 1e-8, 1, None, None) == EINVAL
+    q.p, q.g, q.m, q.v, q.p_type, q.g_type = A, B, C, D, 1, 1
+    buf = (ctypes.c_uint64 * 256)()
+    for n, st in ((-1, EINVAL), (1 << 40, EINVAL), (1 << 37, EINVAL), ((1 << 36) - 4096, OK)):
+        q.n = n
+        assert L.logra_adamw_table(1, arr, buf, 2048) == st, n
 
 
-def test_adamw_nothing_to_do(L):
-    assert _adamw(L, n=0, items=0) == OK
-    assert _adamw(L, n=3, p=None, g=None, m=None, v=None) == OK      # empty tensors
+def _step(L, table, dev=W, lr=1e-3, b1=0.9, b2=0.999, eps=1e-8, step=1, scale=None):
+    return L.logra_adamw_step(table, dev, lr, b1, b2, eps, step, scale, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(lr=-1.0), dict(lr=NAN), dict(lr=INF), dict(b1=1.0), dict(b1=-0.1), dict(b2=1.0),
+    dict(b2=NAN), dict(b2=1.0 - 1e-12), dict(eps=-1e-8), dict(eps=INF), dict(step=0),
+    dict(scale=E + 2), dict(dev=None), dict(dev=W + 4),
+])
+def test_adamw_step_rejects(L, kw):
+    st, buf = _table(L)
+    assert st == OK
+    assert _step(L, ctypes.addressof(buf), **kw) == EINVAL
+
+
+def test_adamw_step_needs_a_table_and_work(L):
+    assert _step(L, None) == EINVAL
+    buf = (ctypes.c_uint64 * 256)()
+    assert _step(L, ctypes.addressof(buf)) == EINVAL          # not a table
+    for kw in (dict(n=0, items=0), dict(n=3, p=None, g=None, m=None, v=None)):
+        arr_n = kw.pop("n")
+        arr = (_lib.AdamWItem * 3)()
+        st = L.logra_adamw_table(arr_n, arr, buf, 2048)       # (no entries in any tensor)
+        assert st == OK
+        assert _step(L, ctypes.addressof(buf), dev=None) == OK
+    # a refused table is no table
+    arr = (_lib.AdamWItem * 1)()
+    q = arr[0]
+    q.p, q.g, q.m, q.v, q.p_type, q.g_type, q.n = A, B, C, D, 1, 1, 1 << 37
+    assert L.logra_adamw_table(1, arr, buf, 2048) == EINVAL
+    assert _step(L, ctypes.addressof(buf)) == EINVAL
 
 
 @pytest.mark.parametrize("args,status", [
@@ -213,13 +249,13 @@ def test_binding_refuses_cpu_tensors():
 
 
 @pytest.mark.parametrize("spans,ok", [
-    ([(0, 10, True, "a"), (10, 20, True, "b")], True),
-    ([(0, 10, False, "a"), (0, 10, False, "b")], True),       # shared inputs
-    ([(0, 10, True, "a"), (0, 10, False, "b")], False),
-    ([(0, 10, False, "a"), (4, 6, True, "b")], False),
-    ([(0, 100, False, "a"), (10, 20, False, "b"), (90, 95, True, "c")], False),
-    ([(0, 100, True, "a"), (10, 20, False, "b")], False),
-    ([(0, 0, True, "a"), (0, 10, True, "b")], True),          # empty tensors
+    ([(0, 10, True, ("a", 0)), (10, 20, True, ("b", 0))], True),
+    ([(0, 10, False, ("a", 0)), (0, 10, False, ("b", 0))], True),       # shared inputs
+    ([(0, 10, True, ("a", 0)), (0, 10, False, ("b", 0))], False),
+    ([(0, 10, False, ("a", 0)), (4, 6, True, ("b", 0))], False),
+    ([(0, 100, False, ("a", 0)), (10, 20, False, ("b", 0)), (90, 95, True, ("c", 0))], False),
+    ([(0, 100, True, ("a", 0)), (10, 20, False, ("b", 0))], False),
+    ([(0, 0, True, ("a", 0)), (0, 10, True, ("b", 0))], True),          # empty tensors
 ])
 def test_overlap_check(spans, ok):
     if ok:
