@@ -313,38 +313,54 @@ __device__ __forceinline__ void split8(const float* x, u32x4& hi, u32x4& lo) {
   }
 }
 
-// Elements K .. K + 7 of a row of U (r of them), those past r as zeros.
+// Elements K .. K + 7 of a row of U (r of them) as loaded: fp32 in both parts, bf16
+// in the bits of the first.  VEC: 16-byte loads (r a multiple of 4 in fp32, of 8 in
+// bf16).  Past r other elements of the row stand in, which meet P's zeros there.
+struct URaw {
+  f32x4 v[2];
+};
 template <bool VEC>
-__device__ __forceinline__ void load_u(const float* row, int K, int r, u32x4& hi, u32x4& lo) {
-  float x[8];
-  if (VEC) {
-    const int at = K < r ? K : 0;
-    const f32x4 u = *reinterpret_cast<const f32x4*>(row + at);
-    const f32x4 v = *reinterpret_cast<const f32x4*>(row + at + 4);
+__device__ __forceinline__ URaw load_u(const float* row, int K, int r) {
+  URaw q;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      x[e] = K < r ? u[e] : 0.0f;
-      x[4 + e] = K < r ? v[e] : 0.0f;
+  for (int h = 0; h < 2; ++h) {
+    const int at = K + 4 * h;
+    if constexpr (VEC) {
+      q.v[h] = *reinterpret_cast<const f32x4*>(row + (at < r ? at : 0));
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) q.v[h][e] = row[at + e < r ? at + e : r - 1];
     }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = K + e < r ? row[K + e] : 0.0f;
   }
-  split8(x, hi, lo);
+  return q;
 }
 template <bool VEC>
-__device__ __forceinline__ void load_u(const uint16_t* row, int K, int r, u32x4& hi, u32x4& lo) {
-  if (VEC) {
-    hi = load_bf16x8_masked(row, K, r);
+__device__ __forceinline__ URaw load_u(const uint16_t* row, int K, int r) {
+  URaw q;
+  if constexpr (VEC) {
+    q.v[0] = *reinterpret_cast<const f32x4*>(row + (K < r ? K : 0));
   } else {
+    uint32_t x[8];
 #pragma unroll
-    for (int p = 0; p < 4; ++p) {
-      const uint32_t x0 = K + 2 * p < r ? row[K + 2 * p] : 0;
-      const uint32_t x1 = K + 2 * p + 1 < r ? row[K + 2 * p + 1] : 0;
-      hi[p] = x0 | (x1 << 16);
-    }
+    for (int e = 0; e < 8; ++e) x[e] = row[K + e < r ? K + e : r - 1];
+    u32x4 w;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = x[2 * e] | (x[2 * e + 1] << 16);
+    q.v[0] = __builtin_bit_cast(f32x4, w);
   }
-  lo = u32x4{0, 0, 0, 0};
+  return q;
+}
+// The pair hi, lo of loaded elements (no lo for bf16).
+template <class UT>
+__device__ __forceinline__ void u_pair(const URaw& q, u32x4& hi, u32x4& lo) {
+  if constexpr (sizeof(UT) == 4) {
+    const float x[8] = {q.v[0][0], q.v[0][1], q.v[0][2], q.v[0][3],
+                        q.v[1][0], q.v[1][1], q.v[1][2], q.v[1][3]};
+    split8(x, hi, lo);
+  } else {
+    hi = __builtin_bit_cast(u32x4, q.v[0]);
+    lo = u32x4{0, 0, 0, 0};
+  }
 }
 
 // The pieces of the kernels below: a wave has 16 rows x 64 columns at a time.
@@ -417,101 +433,164 @@ __device__ __forceinline__ u32x4 add_staged(u32x4 v, const float* stage, int r) 
   return v;
 }
 
-// One block, its policies one after the other with U read from memory: P, Y and
-// the policies are loaded once, the product is run for every policy and each row
-// keeps its own, so that only U's latency is paid per policy.  WHOLE, up
-// to rank 64 and with rows of U on 16-byte boundaries: all of U's operands are
-// loaded together; else a step of 32 along the rank at a time.
-template <int RP, class UT, bool VEC, bool WHOLE>
-__device__ __forceinline__ void direct_block(const AdapterArgs& a, int n_split, float c,
-                                             const float* __restrict__ P, int64_t row0, int col0,
-                                             float* stage) {
+// Few rows: eight waves, one block each, of one strip of 64 columns.  The policies
+// among the work-group's 128 rows are listed once, in the order of their first
+// rows, and taken kSlots at a time: their U operands are brought to LDS by all
+// waves together (the next ones already on their way) and each wave runs the
+// product for those that occur in its block, where each row keeps its own.  A batch
+// of many policies so reads a strip of each U once for 128 rows (1000 mixed tokens
+// of eight policies, 4096 x 4096 at rank 64: 20 us; with each wave reading U itself
+// 57 us).  Where strips alone leave CUs without work, the list is dealt to `deal`
+// work-groups, each of which writes the rows of its policies (64 tokens of 33
+// policies at rank 100: 18.7 us, undealt 43; twice the deal 26, for every
+// work-group reads its rows' pieces of P again).
+constexpr int kBlockWaves = 8;
+
+template <int RP, class UT, bool VEC>
+__global__ __launch_bounds__(64 * kBlockWaves, 2) void adapter_block_kernel(
+    AdapterArgs a, int n_split, float c, int deal, const float* __restrict__ P) {
   constexpr int NKS = RP < 32 ? 1 : RP / 32;
   constexpr bool kPair = sizeof(UT) == 4;
-  constexpr bool kWhole = WHOLE && NKS <= 2 && VEC;
-  constexpr int kHeld = kWhole ? NKS : 1;
+  constexpr int kParts = kPair ? 2 : 1;
+  constexpr int kSlots = RP <= 32 ? 4 : RP == 64 ? 2 : 1;
+  constexpr int kFrags = kSlots * NKS * 4;
+  constexpr int kMine = kFrags / kBlockWaves;   // operands a wave brings
+  constexpr int kOperands = kFrags * kParts * 64 * 16;
+  constexpr int kStages = kBlockWaves * 16 * kStageRow * 4;
+  constexpr int kRows = 16 * kBlockWaves;
+  __shared__ __attribute__((aligned(16)))
+  unsigned char shared[kOperands > kStages ? kOperands : kStages];
+  __shared__ int list[kRows];
+  __shared__ int listed;
+  u32x4* const us = reinterpret_cast<u32x4*>(shared);
   const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int m = lane & 15;
   const int g = lane >> 4;
+  const int n_cb = (a.d + 63) / 64;
+  const int share = (int)(blockIdx.x % deal);
+  const int strip = (int)(blockIdx.x / deal);
+  const int64_t rows0 = (int64_t)(strip / n_cb) * kRows;
+  const int col0 = (strip % n_cb) * 64;
   const int lcol = col0 + 8 * (lane & 7);
+  const int64_t row0 = rows0 + 16 * wave;
   const int64_t row = row0 + m;
   const int64_t t = row < a.T ? row : a.T - 1;
+
+  // the policies, by wave 0
+  auto policy_of = [&](int64_t r) LOGRA_INLINE {
+    const int id = r < a.T ? a.adapter[r] : -1;
+    return id < 0 || (int64_t)id >= a.n ? -1 : id;
+  };
+  if (wave == 0) {
+    const int id0 = policy_of(rows0 + lane), id1 = policy_of(rows0 + 64 + lane);
+    uint64_t left0 = __ballot(id0 >= 0), left1 = __ballot(id1 >= 0);
+    int n = 0;
+    for (int turn = 0; left0 | left1; turn = turn + 1 < deal ? turn + 1 : 0) {
+      const int id = left0 ? __builtin_amdgcn_readlane(id0, __builtin_ctzll(left0))
+                           : __builtin_amdgcn_readlane(id1, __builtin_ctzll(left1));
+      left0 &= ~__ballot(id0 == id);
+      left1 &= ~__ballot(id1 == id);
+      if (turn == share) {
+        if (lane == 0) list[n] = id;
+        ++n;
+      }
+    }
+    if (lane == 0) listed = n;
+  }
   u32x4 y[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) y[i] = load_y(a, row0 + (lane >> 3) + 8 * i, lcol);
-  f32x4 p[kHeld][2];
-  auto load_p = [&](int s, f32x4* q) LOGRA_INLINE {
+  f32x4 p[NKS][2];
+#pragma unroll
+  for (int s = 0; s < NKS; ++s) {
     const float* src = p_at<RP>(P, t, 32 * s + 8 * g);
-    q[0] = *reinterpret_cast<const f32x4*>(src);
-    q[1] = *reinterpret_cast<const f32x4*>(src + 4);
-  };
-  if constexpr (kWhole) {
-#pragma unroll
-    for (int s = 0; s < NKS; ++s) load_p(s, p[s]);
+    p[s][0] = *reinterpret_cast<const f32x4*>(src);
+    p[s][1] = *reinterpret_cast<const f32x4*>(src + 4);
   }
-  int id_m = row < a.T ? a.adapter[row] : -1;
-  if (id_m < 0 || (int64_t)id_m >= a.n) id_m = -1;
+  const int id_m = policy_of(row);
   const float sc = id_m >= 0 ? c * a.scale[id_m] : 0.0f;
-  u32x4 ph[kHeld], pl[kHeld];
-  auto pair_p = [&](int s, const f32x4* q, u32x4& hi, u32x4& lo) LOGRA_INLINE {
-    const int K = 32 * s + 8 * g;
-    p_pair<RP>(q[0], q[1], p_at<RP>(P, t, K), a.T * RP, n_split, sc, K, hi, lo);
-  };
-  if constexpr (kWhole) {
+  __syncthreads();
+  const int n = __builtin_amdgcn_readfirstlane(listed);
+  // this work-group writes the row (and reads its P: the others' stand still)
+  bool own = deal == 1 || (share == 0 && id_m < 0);
+  if (deal > 1)
+    for (int i = 0; i < n; ++i) own |= id_m == list[i];
+  const int64_t tp = own ? t : rows0;
+
+  // Operand f of a phase: slot, step, column block.
+  URaw raw[kMine];
+  auto bring = [&](int phase) LOGRA_INLINE {
 #pragma unroll
-    for (int s = 0; s < NKS; ++s) pair_p(s, p[s], ph[s], pl[s]);
+    for (int i = 0; i < kMine; ++i) {
+      const int f = wave + i * kBlockWaves;
+      const int at = phase * kSlots + f / (4 * NKS);
+      if (at >= n) continue;
+      const int id = __builtin_amdgcn_readfirstlane(list[at]);
+      const int col = col0 + 16 * (f & 3) + m;
+      const UT* urow = static_cast<const UT*>(a.U) + (int64_t)id * a.d * a.r +
+                       (int64_t)(col < a.d ? col : a.d - 1) * a.r;
+      raw[i] = load_u<VEC>(urow, 32 * ((f >> 2) % NKS) + 8 * g, a.r);
+    }
+  };
+  if (n > 0) bring(0);
+  u32x4 ph[NKS], pl[NKS];
+  // (a piece's loads all at once: 200 rows at rank 256 in 39 us, one after the other 45)
+  for (int i = 1; i < n_split; ++i) {
+    f32x4 q[NKS][2];
+#pragma unroll
+    for (int s = 0; s < NKS; ++s) {
+      const float* src = p_at<RP>(P, i * a.T + tp, 32 * s + 8 * g);
+      q[s][0] = *reinterpret_cast<const f32x4*>(src);
+      q[s][1] = *reinterpret_cast<const f32x4*>(src + 4);
+    }
+#pragma unroll
+    for (int s = 0; s < NKS; ++s) {
+      p[s][0] += q[s][0];
+      p[s][1] += q[s][1];
+    }
   }
+#pragma unroll
+  for (int s = 0; s < NKS; ++s)
+    p_pair<RP>(p[s][0], p[s][1], nullptr, 0, 1, sc, 32 * s + 8 * g, ph[s], pl[s]);
   f32x4 sum[4];
 #pragma unroll
   for (int w = 0; w < 4; ++w) sum[w] = f32x4{0.f, 0.f, 0.f, 0.f};
-  uint64_t left = __ballot(id_m >= 0);
-  while (left) {
-    const int id = __builtin_amdgcn_readlane(id_m, __ffsll((unsigned long long)left) - 1);
-    const bool mine = id_m == id;
-    left &= ~__ballot(mine);
-    const UT* U = static_cast<const UT*>(a.U) + (int64_t)id * a.d * a.r;
-    f32x4 v[4];
+  for (int phase = 0; phase * kSlots < n; ++phase) {
 #pragma unroll
-    for (int w = 0; w < 4; ++w) v[w] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto u_row = [&](int w) LOGRA_INLINE {
-      const int col = col0 + 16 * w + m;
-      return U + (int64_t)(col < a.d ? col : a.d - 1) * a.r;
-    };
-    auto product = [&](int w, const u32x4& uh, const u32x4& ul, const u32x4& hi, const u32x4& lo)
-                       LOGRA_INLINE {
-      v[w] = mfma16(uh, lo, v[w]);
-      if constexpr (kPair) v[w] = mfma16(ul, hi, v[w]);
-      v[w] = mfma16(uh, hi, v[w]);
-    };
-    if constexpr (kWhole) {
-      u32x4 uh[NKS][4], ul[NKS][4];
+    for (int i = 0; i < kMine; ++i) {
+      const int f = wave + i * kBlockWaves;
+      u32x4 hi, lo;
+      u_pair<UT>(raw[i], hi, lo);
+      us[f * kParts * 64 + lane] = hi;
+      if constexpr (kPair) us[(f * kParts + 1) * 64 + lane] = lo;
+    }
+    __syncthreads();
+    if ((phase + 1) * kSlots < n) bring(phase + 1);
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
+    for (int j = 0; j < kSlots; ++j) {
+      const int at = phase * kSlots + j;
+      const int id = at < n ? __builtin_amdgcn_readfirstlane(list[at < n ? at : 0]) : -2;
+      const bool mine = id_m == id;
+      if (__ballot(mine) == 0) continue;
 #pragma unroll
-        for (int s = 0; s < NKS; ++s)
-          load_u<VEC>(u_row(w), 32 * s + 8 * g, a.r, uh[s][w], ul[s][w]);
+      for (int w = 0; w < 4; ++w) {
+        f32x4 v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
-#pragma unroll
-        for (int s = 0; s < NKS; ++s) product(w, uh[s][w], ul[s][w], ph[s], pl[s]);
-    } else {
-#pragma unroll 1
-      for (int s = 0; s < NKS; ++s) {
-        load_p(s, p[0]);
-        pair_p(s, p[0], ph[0], pl[0]);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          u32x4 uh, ul;
-          load_u<VEC>(u_row(w), 32 * s + 8 * g, a.r, uh, ul);
-          product(w, uh, ul, ph[0], pl[0]);
+        for (int s = 0; s < NKS; ++s) {
+          const u32x4* u = us + ((j * NKS + s) * 4 + w) * kParts * 64 + lane;
+          const u32x4 uh = u[0];
+          v = mfma16(uh, pl[s], v);
+          if constexpr (kPair) v = mfma16(u[64], ph[s], v);
+          v = mfma16(uh, ph[s], v);
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[w][e] = mine ? v[e] : sum[w][e];
       }
     }
-#pragma unroll
-    for (int w = 0; w < 4; ++w)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) sum[w][e] = mine ? v[w][e] : sum[w][e];
+    __syncthreads();     // the operands' places are free
   }
+  float* const stage = reinterpret_cast<float*>(shared) + wave * 16 * kStageRow;
   stage_sums(stage, sum);
 #pragma unroll
   for (int i = 0; i < 2; ++i) {
@@ -519,19 +598,8 @@ __device__ __forceinline__ void direct_block(const AdapterArgs& a, int n_split, 
     const int id = __shfl(id_m, r);
     // (a row without a policy keeps its bits)
     const u32x4 v = id >= 0 ? add_staged(y[i], stage, r) : y[i];
-    if (row0 + r < a.T) store_out(a, row0 + r, lcol, v);
+    if (__shfl((int)own, r) && row0 + r < a.T) store_out(a, row0 + r, lcol, v);
   }
-  wave_sync();
-}
-
-// Few rows: one wave, one block.
-template <int RP, class UT, bool VEC>
-__global__ __launch_bounds__(64) void adapter_block_kernel(AdapterArgs a, int n_split, float c,
-                                                           const float* __restrict__ P) {
-  __shared__ __attribute__((aligned(16))) float stage[16 * kStageRow];
-  const int n_cb = (a.d + 63) / 64;
-  direct_block<RP, UT, VEC, true>(a, n_split, c, P, (int64_t)(blockIdx.x / n_cb) * 16,
-                                  (int)(blockIdx.x % n_cb) * 64, stage);
 }
 
 // Many rows, rank up to 64 and rows of U on 16-byte boundaries: four waves side by
@@ -604,7 +672,8 @@ __global__ __launch_bounds__(256, 2) void adapter_rows_kernel(AdapterArgs a, int
       const int col = col0 + 16 * w + m;
       const UT* urow = U + (int64_t)(col < a.d ? col : a.d - 1) * a.r;
 #pragma unroll
-      for (int s = 0; s < NKS; ++s) load_u<true>(urow, 32 * s + 8 * g, a.r, uh[s][w], ul[s][w]);
+      for (int s = 0; s < NKS; ++s)
+        u_pair<UT>(load_u<true>(urow, 32 * s + 8 * g, a.r), uh[s][w], ul[s][w]);
     }
   };
   auto compute = [&](int b, const f32x4 (*q)[2], const u32x4* yv) LOGRA_INLINE {
@@ -694,8 +763,8 @@ __global__ __launch_bounds__(256, 2) void adapter_rows_kernel(AdapterArgs a, int
 // Many rows otherwise: eight waves share a strip of 64 columns and take every
 // eighth of its blocks, up to kStripBlocks each.  U's operands of one policy at a
 // time lie in LDS in operand order (converted once for the work-group's rows, 64
-// KB at r = 256 in fp32).  Blocks whose rows belong to several policies (or to
-// none, where they have to be copied) go through direct_block instead, once.
+// KB at r = 256 in fp32).  A block of several policies is run for each of them, in
+// turn, and each time only the rows of that one are written.
 constexpr int kStripBlocks = 8;
 constexpr int kStripWaves = 8;
 
@@ -706,7 +775,6 @@ __global__ __launch_bounds__(64 * kStripWaves, 2) void adapter_strip_kernel(Adap
   constexpr int NKS = RP < 32 ? 1 : RP / 32;
   constexpr bool kPair = sizeof(UT) == 4;
   constexpr int kParts = kPair ? 2 : 1;
-  constexpr bool kAhead = RP <= 128;    // P of a larger rank is not held ahead
   constexpr int kSets = kStripBlocks / 4;
   __shared__ u32x4 us[NKS * 4 * kParts * 64];
   __shared__ __attribute__((aligned(16))) float stage_all[kStripWaves][16 * kStageRow];
@@ -724,12 +792,10 @@ __global__ __launch_bounds__(64 * kStripWaves, 2) void adapter_strip_kernel(Adap
   const int64_t rb0 = (int64_t)group * (kBlockRows * n_blocks) + 16 * wave;
   const int lcol = col0 + 8 * (lane & 7);
 
-  // policies and factors of the wave's rows, 64 to a register; `left`: rows of
-  // the blocks with one policy, `apart`: the other blocks to do (bit b)
+  // policies and factors of the wave's rows, 64 to a register
   int ids[kSets];
   float scs[kSets];
-  uint64_t left[kSets];
-  uint32_t apart = 0;
+  uint64_t left[kSets], none[kSets];
 #pragma unroll
   for (int i = 0; i < kSets; ++i) {
     const int b = 4 * i + (lane >> 4);
@@ -737,19 +803,8 @@ __global__ __launch_bounds__(64 * kStripWaves, 2) void adapter_strip_kernel(Adap
     const bool in = b < n_blocks && row < a.T;
     const int id = in ? a.adapter[row] : -1;
     ids[i] = id < 0 || (int64_t)id >= a.n ? -1 : id;
-    const uint64_t rows = __ballot(in);
-    const uint64_t odd = __ballot(in && ids[i] != __shfl(ids[i], lane & 48));
     left[i] = __ballot(ids[i] >= 0);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint64_t block = uint64_t(0xFFFF) << (16 * j);
-      // (rows that go in place need no copy)
-      const bool alike = (odd & block) == 0 && ((left[i] & block) != 0 || a.out == a.Y);
-      if ((rows & block) != 0 && !alike) {
-        apart |= 1u << (4 * i + j);
-        left[i] &= ~block;
-      }
-    }
+    none[i] = __ballot(in) & ~left[i];
   }
 #pragma unroll
   for (int i = 0; i < kSets; ++i) scs[i] = ids[i] >= 0 ? c * a.scale[ids[i]] : 0.0f;
@@ -767,9 +822,19 @@ __global__ __launch_bounds__(64 * kStripWaves, 2) void adapter_strip_kernel(Adap
       need |= ((rows[b / 4] >> (16 * (b & 3))) & 0xFFFFu) ? 1u << b : 0u;
     return need;
   };
-  for (; apart; apart &= apart - 1)
-    direct_block<RP, UT, VEC, false>(a, n_split, c, P, rb0 + kBlockRows * __builtin_ctz(apart), col0,
-                                     stage);
+  if (a.out != a.Y) {      // rows without a policy are copied
+    for (uint32_t need = blocks_of(none); need; need &= need - 1) {
+      const int b = __builtin_ctz(need);
+      const uint32_t rows = (uint32_t)(of_set(b, none) >> (16 * (b & 3)));
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int r = (lane >> 3) + 8 * i;
+        const int64_t row = rb0 + kBlockRows * b + r;
+        const u32x4 v = load_y(a, row, lcol);
+        if ((rows >> r) & 1) store_out(a, row, lcol, v);
+      }
+    }
+  }
 
   for (;;) {
     // the work-group's next policy: the first one left in its first wave with any
@@ -789,7 +854,8 @@ __global__ __launch_bounds__(64 * kStripWaves, 2) void adapter_strip_kernel(Adap
       const int s = f >> 2;
       const int col = col0 + 16 * (f & 3) + m;
       u32x4 hi, lo;
-      load_u<VEC>(U + (int64_t)(col < a.d ? col : a.d - 1) * a.r, 32 * s + 8 * g, a.r, hi, lo);
+      u_pair<UT>(load_u<VEC>(U + (int64_t)(col < a.d ? col : a.d - 1) * a.r, 32 * s + 8 * g, a.r),
+                 hi, lo);
       us[f * kParts * 64 + lane] = hi;
       if constexpr (kPair) us[(f * kParts + 1) * 64 + lane] = lo;
     }
@@ -798,7 +864,7 @@ __global__ __launch_bounds__(64 * kStripWaves, 2) void adapter_strip_kernel(Adap
     uint64_t mine[kSets];
 #pragma unroll
     for (int i = 0; i < kSets; ++i) {
-      mine[i] = __ballot(ids[i] == id) & left[i];
+      mine[i] = __ballot(ids[i] == id);
       left[i] &= ~mine[i];
     }
     uint32_t need = blocks_of(mine);
@@ -806,17 +872,15 @@ __global__ __launch_bounds__(64 * kStripWaves, 2) void adapter_strip_kernel(Adap
     uint32_t order = 0;    // four bits for each block to do
     for (int j = 0; need; ++j, need &= need - 1) order |= (uint32_t)__builtin_ctz(need) << (4 * j);
 
-    f32x4 p[2][kAhead ? NKS : 1][2];
+    f32x4 p[2][NKS][2];
     u32x4 y[4][2];
     auto load_p = [&](int b, f32x4 (*q)[2]) LOGRA_INLINE {
-      if constexpr (kAhead) {
-        const int64_t row = rb0 + kBlockRows * b + m;
+      const int64_t row = rb0 + kBlockRows * b + m;
 #pragma unroll
-        for (int s = 0; s < NKS; ++s) {
-          const float* src = p_at<RP>(P, row < a.T ? row : a.T - 1, 32 * s + 8 * g);
-          q[s][0] = *reinterpret_cast<const f32x4*>(src);
-          q[s][1] = *reinterpret_cast<const f32x4*>(src + 4);
-        }
+      for (int s = 0; s < NKS; ++s) {
+        const float* src = p_at<RP>(P, row < a.T ? row : a.T - 1, 32 * s + 8 * g);
+        q[s][0] = *reinterpret_cast<const f32x4*>(src);
+        q[s][1] = *reinterpret_cast<const f32x4*>(src + 4);
       }
     };
     auto load_rows = [&](int b, u32x4* v) LOGRA_INLINE {
@@ -833,16 +897,8 @@ __global__ __launch_bounds__(64 * kStripWaves, 2) void adapter_strip_kernel(Adap
       for (int s = 0; s < NKS; ++s) {
         const int K = 32 * s + 8 * g;
         const float* src = p_at<RP>(P, row < a.T ? row : a.T - 1, K);
-        f32x4 v0, v1;
-        if constexpr (kAhead) {
-          v0 = q[s][0];
-          v1 = q[s][1];
-        } else {
-          v0 = *reinterpret_cast<const f32x4*>(src);
-          v1 = *reinterpret_cast<const f32x4*>(src + 4);
-        }
         u32x4 ph, pl;
-        p_pair<RP>(v0, v1, src, a.T * RP, n_split, sc, K, ph, pl);
+        p_pair<RP>(q[s][0], q[s][1], src, a.T * RP, n_split, sc, K, ph, pl);
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
           const u32x4 uh = us[((s * 4 + w) * kParts) * 64 + lane];
@@ -927,15 +983,20 @@ void launch_expand(const AdapterArgs& a, const AdapterPlan& p, float c, const fl
     }
     return;
   }
-  hipLaunchKernelGGL((adapter_block_kernel<RP, UT, VEC>), dim3((unsigned)(blocks * n_cb)), dim3(64),
-                     0, s, a, p.n_split, c, P);
+  const int64_t base = (blocks + kBlockWaves - 1) / kBlockWaves * n_cb;
+  int64_t deal = 2 * kCus / base;
+  if (deal > a.n) deal = a.n;
+  if (deal > a.T) deal = a.T;
+  if (deal < 1) deal = 1;
+  hipLaunchKernelGGL((adapter_block_kernel<RP, UT, VEC>), dim3((unsigned)(base * deal)),
+                     dim3(64 * kBlockWaves), 0, s, a, p.n_split, c, (int)deal, P);
 }
 
 template <int RP>
 void launch_both(const AdapterArgs& a, bool u_f32, const AdapterPlan& p, float c, float* P,
                  hipStream_t s) {
   launch_project<RP>(a, p, P, s);
-  const bool vec = a.r % 8 == 0 && (reinterpret_cast<uintptr_t>(a.U) & 15) == 0;
+  const bool vec = a.r % (u_f32 ? 4 : 8) == 0 && (reinterpret_cast<uintptr_t>(a.U) & 15) == 0;
   if (u_f32) {
     if (vec)
       launch_expand<RP, float, true>(a, p, c, P, s);

@@ -97,6 +97,10 @@ SHAPES = [
     (4100, 264, 1100, 64, 5, "runs"), (4099, 2500, 1096, 256, 3, "runs"),
     (3000, 136, 1501, 100, 4, "mixed"), (3001, 300, 1500, 128, 9, "runs"),
     (9000, 520, 260, 32, 40, "runs"), (2100, 5000, 1024, 16, 2, "one"),
+    # few rows of many policies: rows in whole fp32 lines, but not in bf16
+    (40, 264, 640, 12, 40, "mixed"), (20, 520, 300, 36, 20, "mixed"), (5, 136, 70, 132, 3, "mixed"),
+    (1, 600, 1030, 252, 1, "one"), (130, 264, 2050, 20, 12, "mixed"),
+    (200, 5000, 520, 200, 7, "mixed"), (128, 300, 64, 64, 128, "mixed"),
 ]
 
 
