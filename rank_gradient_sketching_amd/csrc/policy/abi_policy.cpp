@@ -31,17 +31,21 @@ bool ld_ok(int64_t ld, int64_t row, int type) {
   return ld >= row && ld % (16 / bytes_of(type)) == 0 && ld < kLdLimit;
 }
 
-// Bytes [lo, hi) that a matrix of `rows` x `cols` elements spans.
+// Bytes [lo, hi) that a matrix of `rows` x `cols` elements spans.  One that passes
+// the address space (strides reach 2^40) ends at kNoEnd and overlaps everything,
+// which refuses it.
 struct Span {
   uintptr_t lo, hi;
 };
-Span span(const void* p, int64_t rows, int64_t cols, int64_t ld, int64_t elem) {
+constexpr uintptr_t kNoEnd = ~uintptr_t(0);
+Span span(const void* p, __int128 rows, __int128 cols, __int128 ld, int64_t elem) {
   const uintptr_t lo = reinterpret_cast<uintptr_t>(p);
-  return Span{lo, p == nullptr || rows == 0 || cols == 0
-                      ? lo
-                      : lo + (uintptr_t)(((rows - 1) * ld + cols) * elem)};
+  if (p == nullptr || rows == 0 || cols == 0) return Span{lo, lo};
+  const __int128 hi = (__int128)lo + ((rows - 1) * ld + cols) * elem;
+  return Span{lo, hi >= (__int128)kNoEnd ? kNoEnd : (uintptr_t)hi};
 }
 bool overlap(const Span& a, const Span& b) {
+  if (a.hi == kNoEnd || b.hi == kNoEnd) return true;
   return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi;
 }
 
@@ -119,7 +123,8 @@ int logra_token_logprob_backward(const void* z, int dtype, int64_t n_tok, int64_
     return LOGRA_EINVAL;
   const int64_t e = bytes_of(dtype);
   const Span out = span(dz, n_tok, vocab, ldz, e);
-  if (!(dz == z && ldz == ld) && overlap(out, span(z, n_tok, vocab, ld, e))) return LOGRA_EINVAL;
+  const Span in = span(z, n_tok, vocab, ld, e);
+  if (out.hi == kNoEnd || (!(dz == z && ldz == ld) && overlap(out, in))) return LOGRA_EINVAL;
   const void* rows[5] = {lse, d_entropy ? entropy : nullptr, d_logp, d_entropy, d_lse};
   for (const void* q : rows)
     if (overlap(out, span(q, 1, n_tok, 0, 4))) return LOGRA_EINVAL;
@@ -279,7 +284,7 @@ int logra_adapter_apply(const uint16_t* X, int64_t ldx, const uint16_t* Y, int64
   const Span y = span(Y, T, d, ldy, 2);
   if (!(out == Y && ldo == ldy) && overlap(o, y)) return LOGRA_EINVAL;
   const Span in[7] = {span(X, T, k, ldx, 2),
-                      span(U, 1, n * d * r, 0, bytes_of(u_type)),
+                      span(U, n * d, r, r, bytes_of(u_type)),
                       span(A, n * r, k, lda, 2),
                       span(adapter, 1, T, 0, 4),
                       span(scale, 1, n, 0, 4),

@@ -58,6 +58,9 @@ def _lp(L, **kw):
     # outputs that overlap each other, the logits or the workspace
     (dict(H=A), EINVAL), (dict(lse=A + 4), EINVAL), (dict(logp=Z), EINVAL),
     (dict(top=D), EINVAL), (dict(top=W), EINVAL), (dict(logp=T), EINVAL),
+    # strides whose last row lies past the address space
+    (dict(n=1 << 30, ld=1 << 39, dtype=1, n_top=0), EINVAL),
+    (dict(n=(1 << 24) + 1, ld=1 << 39, n_top=0), EINVAL),
 ])
 def test_logprob_rejects(L, kw, status):
     assert _lp(L, **kw) == status
@@ -87,6 +90,9 @@ def _grad(L, **kw):
     dict(target=T + 4),
     # dz over the logits with another stride, or partly, or over a row vector
     dict(dz=Z, ldz=1008), dict(dz=Z + 16), dict(lse=W), dict(dl=W + 4), dict(target=W),
+    # strides whose last row lies past the address space
+    dict(n=(1 << 24) + 1, ld=1 << 39), dict(n=(1 << 24) + 1, ldz=1 << 39),
+    dict(n=(1 << 24) + 1, ldz=1 << 39, ld=1 << 39, dz=Z),
 ])
 def test_logprob_grad_rejects(L, kw):
     assert _grad(L, **kw) == EINVAL
@@ -210,6 +216,11 @@ def _ad(L, **kw):
     (dict(out=T, ldo=520), EINVAL), (dict(out=T + 16), EINVAL), (dict(out=Z), EINVAL),
     (dict(out=C + 16), EINVAL), (dict(adapter=A), EINVAL), (dict(ws=A), EINVAL),
     (dict(ws=Z), EINVAL), (dict(ws=T), EINVAL), (dict(scale=W + 64), EINVAL),
+    # sizes and strides that pass the address space
+    (dict(T=(1 << 24) + 1, ldx=1 << 39, d=8, ldy=8, ldo=8, ws_bytes=1 << 38), EINVAL),
+    (dict(T=(1 << 24) + 1, ldy=1 << 39, ldo=1 << 39, out=T, d=8, ws_bytes=1 << 38), EINVAL),
+    (dict(n=1 << 30, d=1 << 26, ldy=1 << 26, ldo=1 << 26), EINVAL),
+    (dict(seeds=None, A=D, lda=1 << 39, n=1 << 21), EINVAL),
 ])
 def test_adapter_rejects(L, kw, status):
     assert _ad(L, **kw) == status
