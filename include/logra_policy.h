@@ -59,7 +59,7 @@ size_t logra_token_logprob_ws_bytes(int64_t n_tok, int64_t vocab, int32_t n_top)
  *     vocab, ld % 8 == 0 (LOGRA_F32: ld % 4 == 0), 16-B aligned.
  * target: device int64[n_tok], 8-B aligned, or NULL: no row is left out, and
  *     logp must be NULL.
- * tau > 0 and finite; 0 <= n_top <= LOGRA_MAX_TOP.
+ * tau > 0, tau and 1.5 / tau finite; 0 <= n_top <= LOGRA_MAX_TOP.
  * logp, entropy, lse: device float[n_tok] or NULL, where not wanted.
  * top_idx: device int32[n_tok x n_top], top_logp: device float[n_tok x n_top];
  *     not inspected when n_top is 0.
@@ -174,8 +174,8 @@ int logra_adamw_table(int32_t n, const logra_adamw_item* items, void* table, siz
  *
  * table: host memory as logra_adamw_table left it; table_dev: device copy of the
  *     same bytes, 8-B aligned (not inspected when there is nothing to do).
- * lr, beta1, beta2, eps finite; beta in [0, 1) as a float; lr, eps >= 0; step >=
- *     1.
+ * lr, beta1, beta2, eps finite; beta in [0, 1) as a float; lr, eps >= 0 (with eps 0 an
+ *     entry whose v is zero becomes NaN); step >= 1.
  * Returns LOGRA_OK, LOGRA_EINVAL or LOGRA_EHIP.
  */
 int logra_adamw_step(const void* table, const void* table_dev, double lr, double beta1,
@@ -197,7 +197,7 @@ int logra_adamw_state_values(int which, const uint8_t* codes, const uint8_t* exp
                              uint16_t* out, hipStream_t s);
 
 /* Bytes of workspace logra_adapter_apply needs.  Returns 0 for invalid sizes
- * and for T == 0. */
+ * (also past what one launch covers, about T d = 5 10^11) and for T == 0. */
 size_t logra_adapter_ws_bytes(int64_t T, int64_t d, int64_t k, int32_t r);
 
 /*
@@ -211,8 +211,10 @@ size_t logra_adapter_ws_bytes(int64_t T, int64_t d, int64_t k, int32_t r);
  * merged weights for a Y = X W^T of the shared ones, so that requests of
  * several policy versions run as one batch and a proposal's logits can be
  * formed with W left alone.  Rows of one policy need not be adjacent (tiles of
- * 16 rows with one policy are fastest).  P = X A^T is held in fp32 and enters
- * the second product as a bf16 pair of 16 significant bits, and so do fp32 U.
+ * 32 rows with one policy are fastest).  P = X A^T is held in fp32 and enters
+ * the second product as a bf16 pair of 16 significant bits, and so do fp32 U
+ * (infinities, and values within 2^-9 of fp32's largest, come out as NaN).  A NaN
+ * or an infinity in a row's X touches that row alone, one in a policy its rows.
  *
  * X: device bf16[T x ldx], k columns; Y, out: device bf16[T x ldy] / [T x
  *     ldo], d columns; ld rules of logra.h.  out may be Y itself with the same

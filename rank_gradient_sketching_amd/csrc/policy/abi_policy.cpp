@@ -26,6 +26,8 @@ bool aligned(const void* p, uintptr_t a) {
 bool dim_ok(int64_t x) { return x >= 1 && x < kDimLimit; }
 bool type_ok(int t) { return t == LOGRA_BF16 || t == LOGRA_F32; }
 int64_t bytes_of(int type) { return type == LOGRA_F32 ? 4 : 2; }
+// 1 / tau and log2(e) / tau stay finite.
+bool tau_ok(float tau) { return isfinite(tau) && tau > 0.0f && isfinite(1.5f / tau); }
 // Row stride: >= row length, rows on 16-byte boundaries.
 bool ld_ok(int64_t ld, int64_t row, int type) {
   return ld >= row && ld % (16 / bytes_of(type)) == 0 && ld < kLdLimit;
@@ -74,7 +76,7 @@ int logra_token_logprob(const void* z, int dtype, int64_t n_tok, int64_t vocab, 
                         size_t ws_bytes, hipStream_t s) {
   if (!type_ok(dtype) || !dim_ok(vocab) || n_tok < 0 || n_tok >= kDimLimit) return LOGRA_EINVAL;
   if (n_top < 0 || n_top > LOGRA_MAX_TOP) return LOGRA_EINVAL;
-  if (!isfinite(tau) || !(tau > 0.0f)) return LOGRA_EINVAL;
+  if (!tau_ok(tau)) return LOGRA_EINVAL;
   if (!ld_ok(ld, vocab, dtype)) return LOGRA_EINVAL;
   if (n_tok == 0) return LOGRA_OK;
   if (z == nullptr || !aligned(z, 16)) return LOGRA_EINVAL;
@@ -110,7 +112,7 @@ int logra_token_logprob_backward(const void* z, int dtype, int64_t n_tok, int64_
                                  const float* d_entropy, const float* d_lse, void* dz,
                                  int64_t ldz, hipStream_t s) {
   if (!type_ok(dtype) || !dim_ok(vocab) || n_tok < 0 || n_tok >= kDimLimit) return LOGRA_EINVAL;
-  if (!isfinite(tau) || !(tau > 0.0f)) return LOGRA_EINVAL;
+  if (!tau_ok(tau)) return LOGRA_EINVAL;
   if (!ld_ok(ld, vocab, dtype) || !ld_ok(ldz, vocab, dtype)) return LOGRA_EINVAL;
   if (n_tok == 0) return LOGRA_OK;
   if (z == nullptr || dz == nullptr || lse == nullptr) return LOGRA_EINVAL;

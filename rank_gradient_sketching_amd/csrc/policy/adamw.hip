@@ -22,9 +22,10 @@
 // Bound: HBM bytes (a bf16 weight with fp32 master, bf16 gradient and fp32
 // states moves 28 bytes an entry, 8-bit states 16).  A work-group takes 4096
 // consecutive entries of one tensor, every load of its four steps issued
-// before the first is used.  The tensors of a launch travel in its argument
-// block (48 at most), where a work-group finds its own by comparing all
-// tensors' first chunks at once, one per lane.
+// before the first is used.  The tensors stand in a table in device memory,
+// where a work-group finds its own by comparing 64 tensors' first work-groups
+// at once, one per lane (a level more for every 64 times as many).  All tensors
+// of a form are one launch: 140 small ones take 4.0 us.
 #include <math.h>
 
 #include <type_traits>

@@ -1031,7 +1031,9 @@ bool make_adapter_plan(int64_t T, int64_t d, int64_t k, int r, AdapterPlan* p) {
   p->total = (size_t)round_up((int64_t)p->n_split * T * p->rp * 4, 256);
   // (flat grids: work-groups, and threads below 2^32)
   const int64_t most = (int64_t(1) << 24) - 1;
-  return tiles * p->n_split <= most / 2 && (T + 63) / 64 * ((d + 63) / 64) / 16 <= most / 2;
+  return tiles * p->n_split <= most / 2 &&                                     // project
+         (T + 255) / 256 * ((d + 255) / 256) <= most &&                        // rows
+         (T + 1023) / 1024 * ((d + 63) / 64) <= most / 2;                      // strip
 }
 
 hipError_t launch_adapter(const AdapterArgs& a, bool u_f32, const AdapterPlan& p, char* ws,

@@ -227,7 +227,8 @@ def adamw_bind(params, grads, m, v, master=None, m_exp=None, v_exp=None, weight_
     entries); weight_decay: one number or a list.  All contiguous, on one GPU.
     The handle keeps the storage that the tensors have now and steps that:
     bind again after giving a tensor other storage (e.g. a new gradient).  It
-    copies a table to the GPU, so it is made outside a stream capture."""
+    copies a table to the GPU, so it is made outside a stream capture, and is
+    kept until its steps have run (a captured one: as long as its graph)."""
     params = list(params)
     n = len(params)
     if n == 0:

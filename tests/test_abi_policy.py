@@ -51,6 +51,7 @@ def _lp(L, **kw):
     (dict(ld=10004), EINVAL), (dict(dtype=1, ld=10002), EINVAL), (dict(target=None), EINVAL),
     (dict(target=T + 4), EINVAL), (dict(tau=0.0), EINVAL), (dict(tau=NAN), EINVAL),
     (dict(tau=INF), EINVAL), (dict(tau=-1.0), EINVAL), (dict(n_top=-1), EINVAL),
+    (dict(tau=1e-39), EINVAL),                      # log2(e) / tau past fp32
     (dict(n_top=65), EINVAL), (dict(logp=A + 2), EINVAL), (dict(H=B + 1), EINVAL),
     (dict(lse=C + 2), EINVAL), (dict(idx=None), EINVAL), (dict(top=None), EINVAL),
     (dict(idx=D + 2), EINVAL), (dict(ws=None), EWS), (dict(ws_bytes=64), EWS),
@@ -86,7 +87,7 @@ def _grad(L, **kw):
 @pytest.mark.parametrize("kw", [
     dict(z=None), dict(dz=None), dict(lse=None), dict(z=Z + 2), dict(dz=W + 2), dict(ldz=999),
     dict(ldz=1004), dict(dl=None, dh=None, ds=None), dict(target=None), dict(H=None),
-    dict(dtype=3), dict(n=-1), dict(V=0), dict(tau=0.0), dict(lse=A + 2), dict(dl=C + 1),
+    dict(dtype=3), dict(n=-1), dict(V=0), dict(tau=0.0), dict(tau=1e-39), dict(lse=A + 2), dict(dl=C + 1),
     dict(target=T + 4),
     # dz over the logits with another stride, or partly, or over a row vector
     dict(dz=Z, ldz=1008), dict(dz=Z + 16), dict(lse=W), dict(dl=W + 4), dict(target=W),
@@ -235,6 +236,10 @@ def test_adapter_empty_and_sizes(L):
     # flat grids past their limit are refused
     assert L.logra_adapter_ws_bytes((1 << 31) - 1, 4096, 64, 1) == 0
     assert _ad(L, T=(1 << 31) - 1, d=4096, ldy=4096, ldo=4096, out=T) == EINVAL
+    # ... also those of few rows and a very wide layer
+    assert L.logra_adapter_ws_bytes(1, 1 << 30, 64, 1) == 0
+    assert L.logra_adapter_ws_bytes(1, 1 << 28, 64, 1) > 0
+    assert L.logra_adapter_ws_bytes(8192, 1 << 25, 64, 1) > 0
 
 
 # ------------------------------------------------------------------ binding
