@@ -332,3 +332,21 @@ def test_refusals_and_overlaps(lg):
     # empty tensors are left out
     lg.adamw_step(lg.adamw_bind([t(n=0), p], [t(n=0), g], [t(n=0), m], [t(n=0), v]), 1e-3, 1)
     assert p.eq(0).all()
+
+
+@pytest.mark.parametrize("which", ["m", "v"])
+@pytest.mark.parametrize("off", [0, 1])
+def test_state_values_of_every_code(lg, which, off):
+    """All codes under all exponents, in whole vectors and (one entry off) not;
+    the last block is short."""
+    say(f"adamw values {which} off {off}")
+    exps = np.repeat(np.arange(16, 256, dtype=np.uint8), 8)
+    codes = np.tile(np.arange(256, dtype=np.uint8), 240)
+    codes[codes == 128] = 0 if which == "m" else 128     # (the form has no -0)
+    n = codes.size - 5
+    q = torch.zeros(codes.size + off, dtype=torch.uint8, device="cuda")[off:off + n]
+    q.copy_(torch.from_numpy(codes[:n]))
+    out = lg.adamw_state_values(q, torch.from_numpy(exps).cuda(), which)
+    want = oad.decode(codes[:n], exps, which)
+    assert np.array_equal(f64(out), want, equal_nan=True)
+    assert np.isnan(want[-251:]).all() and np.isfinite(want[:-251]).all()
