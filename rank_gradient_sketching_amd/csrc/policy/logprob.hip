@@ -35,7 +35,9 @@
 // Bound: the stream of the logits and, close behind it, the vector unit (eight
 // elements cost about 70 issue slots, 32 of them the exponentials).  One
 // work-group per row where the rows fill the chip; fewer rows are cut into pieces
-// whose states and keys a second kernel joins.
+// whose states and keys a second kernel joins.  4096 x 152064 bf16: 198 us, 6.3
+// TB/s.  8 rows of it with eight alternatives: 8.5 + 6.8 us (5.1 + 3.3 without),
+// 501 x 32003 fp32 likewise 23.5 + 6.4 (15.2 + 3.9).
 #include <math.h>
 
 #include "common.hpp"
@@ -724,7 +726,7 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
 
 // Work-groups a chip full of streaming work wants, and the most a launch takes
 // (tasks beyond it are walked by the same work-groups).
-constexpr int64_t kFill = 512;
+constexpr int64_t kFill = 512;   // (501 x 32003: 28.4 us; 1024 31.7, 2048 32.2, 4096 40)
 constexpr int64_t kMaxGrid = 1 << 20;
 
 template <class T>
