@@ -36,8 +36,8 @@
 // elements cost about 70 issue slots, 32 of them the exponentials).  One
 // work-group per row where the rows fill the chip; fewer rows are cut into pieces
 // whose states and keys a second kernel joins.  4096 x 152064 bf16: 198 us, 6.3
-// TB/s.  8 rows of it with eight alternatives: 8.5 + 6.8 us (5.1 + 3.3 without),
-// 501 x 32003 fp32 likewise 23.5 + 6.4 (15.2 + 3.9).
+// TB/s.  8 rows of it with eight alternatives: 8.4 + 6.2 us (5.1 + 3.3 without),
+// 501 x 32003 fp32 likewise 23.0 + 5.2 (15.2 + 3.9).
 #include <math.h>
 
 #include "common.hpp"
@@ -315,6 +315,13 @@ __device__ __forceinline__ void best_tokens(BestKeys& b, const T* z, int V, int 
   const int lane = threadIdx.x & 63;
   const u64 runs = b.best;
   const int n = __popcll(__ballot(lane < n_top && runs != 0));
+  if (n * GT::kRun <= 64) {
+    const uint32_t lo = __shfl((uint32_t)runs, lane / GT::kRun);
+    const int64_t col = (int64_t)(0xFFFFFFFFu - lo) + lane % GT::kRun;
+    const float x = lane < n * GT::kRun && col < V ? GT::one(z, col) : -INFINITY;
+    b.best = sort_lanes(x > -INFINITY ? order_key(x, (uint32_t)col) : 0, true);
+    return;
+  }
   BestKeys t = no_keys(b.buf);
   // (n_top runs have a token not below the last one's best)
   if (n == n_top)
@@ -439,9 +446,8 @@ __device__ __forceinline__ float log_p(float z, const State& st, float l2t, floa
   return (isfinite(d) ? d : (z - st.m) / tau) - logf(st.s);
 }
 // By one thread of the row.
-template <class T>
 __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, const State& st,
-                                          float l2t) {
+                                          float l2t, float zt) {
   const float ln_s = logf(st.s);
   const float mc = st.m * l2t;
   if (a.lse) {
@@ -450,10 +456,12 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, con
     a.lse[row] = st.m / a.tau + (ln_s - off);
   }
   if (a.entropy) a.entropy[row] = ln_s - kLn2 * (st.u / st.s);
-  if (a.logp) {
-    const float zt = Group<T>::one(static_cast<const T*>(a.z) + row * a.ld, a.target[row]);
-    a.logp[row] = log_p(zt, st, l2t, a.tau);
-  }
+  if (a.logp) a.logp[row] = log_p(zt, st, l2t, a.tau);
+}
+// The target's logit (0 where it is not asked for); the row is not left out.
+template <class T>
+__device__ __forceinline__ float target_logit(const LogprobArgs& a, int64_t row) {
+  return a.logp ? Group<T>::one(static_cast<const T*>(a.z) + row * a.ld, a.target[row]) : 0.0f;
 }
 // By the lanes of one wave of the row.
 __device__ __forceinline__ void write_keys(const LogprobArgs& a, int64_t row, const State& st,
@@ -585,7 +593,7 @@ __global__ __launch_bounds__(kThreads) void logprob_rows_kernel(LogprobArgs a, i
         }
       }
       if (n_split == 1) {
-        if (lane == 0) write_row<T>(a, row, t, l2t);
+        if (lane == 0) write_row(a, row, t, l2t, target_logit<T>(a, row));
         if constexpr (TOP) {
           best_tokens<GT>(bk, z, a.vocab, a.n_top);
           write_keys(a, row, t, l2t, bk.best);
@@ -614,26 +622,49 @@ __global__ __launch_bounds__(64) void logprob_join_kernel(LogprobArgs a, int n_s
   const int lane = threadIdx.x;
   const float l2t = kLog2e / a.tau;
   for (int64_t row = blockIdx.x; row < a.n_tok; row += gridDim.x) {
-    if (left_out(a, row)) continue;
+    // (what the row needs is loaded at once, and keys that fit the lanes are sorted
+    // as they are: 501 rows in 5.2 us, one after the other through LDS 6.5)
+    const int64_t target = a.target ? a.target[row] : 0;
     State st{kMinFloat, 0.0f, 0.0f};
-    for (int i = lane; i < n_split; i += 64) {
-      const float* q = states + 3 * (row * n_split + i);
-      st = merge_states(st, State{q[0], q[1], q[2]}, l2t);
+    const float* sq = states + 3 * row * n_split;
+    if (lane < n_split) st = State{sq[3 * lane], sq[3 * lane + 1], sq[3 * lane + 2]};
+    const int n = n_split * a.n_top;
+    const u64* q = keys + row * n;
+    u64 x0 = 0;
+    // (more than fit the lanes: the pieces' best keys, for a threshold)
+    if constexpr (TOP) {
+      if (n <= 64)
+        x0 = lane < n ? q[lane] : 0;
+      else
+        x0 = lane < n_split ? q[lane * a.n_top] : 0;
     }
+    if (target < 0 || target >= a.vocab) continue;
+    const float zt = target_logit<T>(a, row);
+    for (int i = lane + 64; i < n_split; i += 64)
+      st = merge_states(st, State{sq[3 * i], sq[3 * i + 1], sq[3 * i + 2]}, l2t);
     st = wave_state(st, l2t);
-    if (lane == 0) write_row<T>(a, row, st, l2t);
+    if (lane == 0) write_row(a, row, st, l2t, zt);
     if constexpr (TOP) {
       BestKeys bk = no_keys(buf);
-      // the pieces' best keys first: their n_top-th leaves few others
-      const u64* q = keys + row * n_split * a.n_top;
-      first_threshold(bk, lane < n_split ? (uint32_t)(q[lane * a.n_top] >> 32) : 0, a.n_top);
-      const int n = n_split * a.n_top;
-      for (int i = 0; i < n; i += 64) {
-        const u64 x = i + lane < n ? q[i + lane] : 0;
-        append(bk, x, x != 0);
-        if (bk.count >= 64) flush_keys(bk, 64, a.n_top);
+      if (n <= 64) {
+        bk.best = sort_lanes(x0, true);
+      } else {
+        // the pieces' best keys first: their n_top-th leaves few others
+        first_threshold(bk, (uint32_t)(x0 >> 32), a.n_top);
+        constexpr int kAtOnce = 4;
+        for (int i = 0; i < n; i += 64 * kAtOnce) {
+          u64 x[kAtOnce];
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j)
+            x[j] = i + 64 * j + lane < n ? q[i + 64 * j + lane] : 0;
+#pragma unroll
+          for (int j = 0; j < kAtOnce; ++j) {
+            append(bk, x[j], x[j] != 0);
+            if (bk.count >= 64) flush_keys(bk, 64, a.n_top);
+          }
+        }
+        flush_keys(bk, 1, a.n_top);
       }
-      flush_keys(bk, 1, a.n_top);
       best_tokens<Group<T>>(bk, static_cast<const T*>(a.z) + row * a.ld, a.vocab, a.n_top);
       write_keys(a, row, st, l2t, bk.best);
     }
