@@ -437,16 +437,16 @@ __device__ __forceinline__ u32x4 add_staged(u32x4 v, const float* stage, int r) 
 }
 
 // Few rows: eight waves, one block each, of one strip of 64 columns.  The policies
-// among the work-group's 128 rows are listed once, in the order of their first
-// rows, and taken kSlots at a time: their U operands are brought to LDS by all
-// waves together (the next ones already on their way) and each wave runs the
-// product for those that occur in its block, where each row keeps its own.  A batch
-// of many policies so reads a strip of each U once for 128 rows (1000 mixed tokens
-// of eight policies, 4096 x 4096 at rank 64: 20 us; with each wave reading U itself
-// 57 us).  Where strips alone leave CUs without work, the list is dealt to `deal`
-// work-groups, each of which writes the rows of its policies (64 tokens of 33
-// policies at rank 100: 18.7 us, undealt 43; twice the deal 26, for every
-// work-group reads its rows' pieces of P again).
+// among the work-group's 128 rows, in the order of their first rows, are taken
+// kSlots at a time: their U operands are brought to LDS by all waves together (the
+// next ones already on their way) and each wave runs the product for those that
+// occur in its block, where each row keeps its own.  A batch of many policies so
+// reads a strip of each U once for 128 rows (1000 mixed tokens of eight policies,
+// 4096 x 4096 at rank 64: 20 us; with each wave reading U itself 57 us).  Where
+// strips alone leave CUs without work, the policies are dealt to `deal` work-groups,
+// each of which writes the rows of its own (64 tokens of 33 policies at rank 100:
+// 20 us, undealt 43; twice the deal 26, for every work-group reads its rows' pieces
+// of P again).
 constexpr int kBlockWaves = 8;
 
 template <int RP, class UT, bool VEC>
@@ -463,8 +463,6 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void adapter_block_kernel(
   constexpr int kRows = 16 * kBlockWaves;
   __shared__ __attribute__((aligned(16)))
   unsigned char shared[kOperands > kStages ? kOperands : kStages];
-  __shared__ int list[kRows];
-  __shared__ int listed;
   u32x4* const us = reinterpret_cast<u32x4*>(shared);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -480,27 +478,13 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void adapter_block_kernel(
   const int64_t row = row0 + m;
   const int64_t t = row < a.T ? row : a.T - 1;
 
-  // the policies, by wave 0
+  // The policies of this work-group, one after the other: every wave walks the
+  // rows' list for itself, a phase ahead, so nothing waits for the whole of it.
   auto policy_of = [&](int64_t r) LOGRA_INLINE {
     const int id = r < a.T ? a.adapter[r] : -1;
     return id < 0 || (int64_t)id >= a.n ? -1 : id;
   };
-  if (wave == 0) {
-    const int id0 = policy_of(rows0 + lane), id1 = policy_of(rows0 + 64 + lane);
-    uint64_t left0 = __ballot(id0 >= 0), left1 = __ballot(id1 >= 0);
-    int n = 0;
-    for (int turn = 0; left0 | left1; turn = turn + 1 < deal ? turn + 1 : 0) {
-      const int id = left0 ? __builtin_amdgcn_readlane(id0, __builtin_ctzll(left0))
-                           : __builtin_amdgcn_readlane(id1, __builtin_ctzll(left1));
-      left0 &= ~__ballot(id0 == id);
-      left1 &= ~__ballot(id1 == id);
-      if (turn == share) {
-        if (lane == 0) list[n] = id;
-        ++n;
-      }
-    }
-    if (lane == 0) listed = n;
-  }
+  const int id0 = policy_of(rows0 + lane), id1 = policy_of(rows0 + 64 + lane);
   u32x4 y[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) y[i] = load_y(a, row0 + (lane >> 3) + 8 * i, lcol);
@@ -511,34 +495,59 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void adapter_block_kernel(
     p[s][0] = *reinterpret_cast<const f32x4*>(src);
     p[s][1] = *reinterpret_cast<const f32x4*>(src + 4);
   }
-  const int id_m = policy_of(row);
+  uint64_t left0 = __ballot(id0 >= 0), left1 = __ballot(id1 >= 0);
+  int turn = 0;
+  auto next = [&]() LOGRA_INLINE {
+    int id = -1;
+    while (id < 0 && (left0 | left1)) {
+      id = left0 ? __builtin_amdgcn_readlane(id0, __builtin_ctzll(left0))
+                 : __builtin_amdgcn_readlane(id1, __builtin_ctzll(left1));
+      left0 &= ~__ballot(id0 == id);
+      left1 &= ~__ballot(id1 == id);
+      if (turn != share) id = -1;
+      turn = turn + 1 < deal ? turn + 1 : 0;
+    }
+    return id;
+  };
+  const int id_m = __shfl(wave < 4 ? id0 : id1, 16 * (wave & 3) + m);
   const float sc = id_m >= 0 ? c * a.scale[id_m] : 0.0f;
-  __syncthreads();
-  const int n = __builtin_amdgcn_readfirstlane(listed);
-  // this work-group writes the row (and reads its P: the others' stand still)
-  bool own = deal == 1 || (share == 0 && id_m < 0);
-  if (deal > 1)
-    for (int i = 0; i < n; ++i) own |= id_m == list[i];
-  const int64_t tp = own ? t : rows0;
+  bool own = share == 0 && id_m < 0;      // this work-group writes the row
 
   // Operand f of a phase: slot, step, column block.
+  int cur[kSlots];
   URaw raw[kMine];
-  auto bring = [&](int phase) LOGRA_INLINE {
+  auto bring = [&](const int* ids) LOGRA_INLINE {
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
       const int f = wave + i * kBlockWaves;
-      const int at = phase * kSlots + f / (4 * NKS);
-      if (at >= n) continue;
-      const int id = __builtin_amdgcn_readfirstlane(list[at]);
+      int id = ids[0];
+#pragma unroll
+      for (int j = 1; j < kSlots; ++j) id = f / (4 * NKS) == j ? ids[j] : id;
+      if (id < 0) continue;
       const int col = col0 + 16 * (f & 3) + m;
       const UT* urow = static_cast<const UT*>(a.U) + (int64_t)id * a.d * a.r +
                        (int64_t)(col < a.d ? col : a.d - 1) * a.r;
       raw[i] = load_u<VEC>(urow, 32 * ((f >> 2) % NKS) + 8 * g, a.r);
     }
   };
-  if (n > 0) bring(0);
+#pragma unroll
+  for (int j = 0; j < kSlots; ++j) cur[j] = next();
+  bring(cur);
+  // (dealt: the rest of the walk at once, so that only own rows' P are read)
+  int64_t tp = t;
+  if (deal > 1) {
+    const uint64_t at0 = left0, at1 = left1;
+    const int at_turn = turn;
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) own |= cur[j] >= 0 && id_m == cur[j];
+    for (int id = next(); id >= 0; id = next()) own |= id_m == id;
+    left0 = at0;
+    left1 = at1;
+    turn = at_turn;
+    tp = own ? t : rows0;
+  }
   u32x4 ph[NKS], pl[NKS];
-  // (a piece's loads all at once: 200 rows at rank 256 in 39 us, one after the other 45)
+  // (a piece's loads all at once: 200 rows at rank 256 in 38 us, one after the other 45)
   for (int i = 1; i < n_split; ++i) {
     f32x4 q[NKS][2];
 #pragma unroll
@@ -559,7 +568,7 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void adapter_block_kernel(
   f32x4 sum[4];
 #pragma unroll
   for (int w = 0; w < 4; ++w) sum[w] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int phase = 0; phase * kSlots < n; ++phase) {
+  while (cur[0] >= 0) {
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
       const int f = wave + i * kBlockWaves;
@@ -569,13 +578,15 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void adapter_block_kernel(
       if constexpr (kPair) us[(f * kParts + 1) * 64 + lane] = lo;
     }
     __syncthreads();
-    if ((phase + 1) * kSlots < n) bring(phase + 1);
+    int ahead[kSlots];
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) ahead[j] = next();
+    bring(ahead);
 #pragma unroll
     for (int j = 0; j < kSlots; ++j) {
-      const int at = phase * kSlots + j;
-      const int id = at < n ? __builtin_amdgcn_readfirstlane(list[at < n ? at : 0]) : -2;
-      const bool mine = id_m == id;
+      const bool mine = cur[j] >= 0 && id_m == cur[j];
       if (__ballot(mine) == 0) continue;
+      own |= mine;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         f32x4 v = {0.f, 0.f, 0.f, 0.f};
@@ -592,6 +603,8 @@ __global__ __launch_bounds__(64 * kBlockWaves, 2) void adapter_block_kernel(
       }
     }
     __syncthreads();     // the operands' places are free
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j) cur[j] = ahead[j];
   }
   float* const stage = reinterpret_cast<float*>(shared) + wave * 16 * kStageRow;
   stage_sums(stage, sum);
