@@ -231,7 +231,10 @@ size_t logra_adapter_ws_bytes(int64_t T, int64_t d, int64_t k, int32_t r);
  * ws: device scratch of logra_adapter_ws_bytes(T, d, k, r) bytes, 256-B
  *     aligned.
  * T == 0 is a no-op.  1 <= r <= LOGRA_MAX_RANK, 1 <= n < 2^31, d, k >= 1, all
- * of T, d, k < 2^31.  The result does not depend on the order of the rows.
+ * of T, d, k < 2^31.  The same call gives the same bits.  A row that moves to
+ * another tile of 32 rows, or into a batch of another size, may see its fp32 sums
+ * over k in another order (tiles start at different columns, few tiles are cut
+ * along k); moved inside its tile it keeps its bits.
  * Returns LOGRA_OK, LOGRA_EINVAL, LOGRA_EWORKSPACE or LOGRA_EHIP.
  */
 int logra_adapter_apply(const uint16_t* X, int64_t ldx, const uint16_t* Y, int64_t ldy,

@@ -129,7 +129,8 @@ def test_apply(lg, T, k, d, r, n, rows, signs, u_dtype):
 
 def test_rows_do_not_touch_each_other(lg):
     """NaN and infinite rows, policies and ids out of range: every other row is
-    what it is without them; the order of the rows does not matter."""
+    what it is without them; nor does their order matter where k has two pieces (a
+    sum of two)."""
     say("adapter isolation")
     c = case(50, 300, 200, 16, 5, True, torch.float32, "mixed", seed=1)
     ref = apply(lg, c, out=torch.empty_like(c["Y"])).clone()
@@ -151,6 +152,25 @@ def test_rows_do_not_touch_each_other(lg):
     perm = torch.from_numpy(np.random.default_rng(0).permutation(50)).cuda()
     p = dict(c, X=padded(c["X"][perm].cpu()), Y=padded(c["Y"][perm].cpu()), adapter=c["adapter"][perm].contiguous())
     assert torch.equal(apply(lg, p).contiguous().view(torch.int16), ref[perm].contiguous().view(torch.int16))
+
+
+@pytest.mark.parametrize("signs", [True, False])
+def test_same_bits_again_and_inside_a_tile(lg, signs):
+    """The same call twice, and rows that trade places inside their tiles of 32."""
+    say(f"adapter order inside tiles signs {signs}")
+    for T, k, d, r, n in ((90, 5000, 200, 64, 7), (1100, 2600, 1100, 32, 5)):
+        c = case(T, k, d, r, n, signs, torch.float32, "mixed", seed=T)
+        to = padded(torch.zeros(T, d, dtype=torch.bfloat16))
+        out = lambda q: apply(lg, q, out=to).contiguous().view(torch.int16)
+        ref = out(c).clone()
+        to.zero_()
+        assert torch.equal(out(c), ref)
+        rng = np.random.default_rng(T)
+        perm = np.concatenate([t + rng.permutation(min(32, T - t)) for t in range(0, T, 32)])
+        perm = torch.from_numpy(perm).cuda()
+        p = dict(c, X=padded(c["X"][perm].cpu()), Y=padded(c["Y"][perm].cpu()),
+                 adapter=c["adapter"][perm].contiguous())
+        assert torch.equal(out(p), ref[perm])
 
 
 def test_signed_zeros_and_nan_bits_of_base_rows(lg):
