@@ -224,9 +224,10 @@ size_t logra_adapter_ws_bytes(int64_t T, int64_t d, int64_t k, int32_t r);
  *     aligned to its type.
  * seeds: device uint64[n x 2] (seed, stream) of the sign basis, 8-B aligned;
  *     then c = 1 / sqrt(r) and A must be NULL.
- * A: else device bf16[n x r x lda] (row stride lda, ld rules; policies r lda
- *     apart): the bases themselves (e.g. Gaussian ones made once by
- *     logra_regen_A), c = 1, seeds NULL.
+ * A: else device bf16[n x r x lda] (row stride lda >= k; policies r lda apart;
+ *     2-B aligned, fastest where rows lie on 16-byte boundaries): the bases
+ *     themselves (e.g. Gaussian ones made once by logra_regen_A), c = 1, seeds
+ *     NULL.
  * scale: device float[n], 4-B aligned.
  * ws: device scratch of logra_adapter_ws_bytes(T, d, k, r) bytes, 256-B
  *     aligned.

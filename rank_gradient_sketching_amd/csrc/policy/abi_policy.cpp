@@ -270,7 +270,7 @@ int logra_adapter_apply(const uint16_t* X, int64_t ldx, const uint16_t* Y, int64
   if (!ld_ok(ldx, k, LOGRA_BF16) || !ld_ok(ldy, d, LOGRA_BF16) || !ld_ok(ldo, d, LOGRA_BF16))
     return LOGRA_EINVAL;
   if ((seeds == nullptr) == (A == nullptr)) return LOGRA_EINVAL;
-  if (A != nullptr && (!aligned(A, 16) || !ld_ok(lda, k, LOGRA_BF16))) return LOGRA_EINVAL;
+  if (A != nullptr && (!aligned(A, 2) || lda < k || lda >= kLdLimit)) return LOGRA_EINVAL;
   if (seeds != nullptr && !aligned(seeds, 8)) return LOGRA_EINVAL;
   if (T == 0) return LOGRA_OK;
   if (X == nullptr || Y == nullptr || out == nullptr || adapter == nullptr || U == nullptr ||

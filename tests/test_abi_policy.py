@@ -204,7 +204,7 @@ def _ad(L, **kw):
     (dict(X=None), EINVAL), (dict(Y=None), EINVAL), (dict(out=None), EINVAL),
     (dict(adapter=None), EINVAL), (dict(U=None), EINVAL), (dict(scale=None), EINVAL),
     (dict(seeds=None), EINVAL), (dict(A=Z, lda=256), EINVAL), (dict(seeds=None, A=D), EINVAL),
-    (dict(seeds=None, A=D + 2, lda=256), EINVAL), (dict(seeds=None, A=D, lda=260), EINVAL),
+    (dict(seeds=None, A=D + 1, lda=256), EINVAL), (dict(seeds=None, A=D, lda=255), EINVAL),
     (dict(T=-1), EINVAL), (dict(T=1 << 31), EINVAL), (dict(d=0), EINVAL), (dict(k=0), EINVAL),
     (dict(r=0), EINVAL), (dict(r=257), EINVAL), (dict(n=0), EINVAL), (dict(n=1 << 31), EINVAL),
     (dict(u_type=2), EINVAL), (dict(ldx=255), EINVAL), (dict(ldx=260), EINVAL),

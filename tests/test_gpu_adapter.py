@@ -154,6 +154,25 @@ def test_rows_do_not_touch_each_other(lg):
     assert torch.equal(apply(lg, p).contiguous().view(torch.int16), ref[perm].contiguous().view(torch.int16))
 
 
+@pytest.mark.parametrize("T,k,d,r,n", [(1, 1, 8, 1, 1), (5, 37, 65, 3, 2), (40, 255, 72, 17, 5),
+                                       (70, 1041, 264, 100, 9), (33, 777, 128, 250, 3),
+                                       (612, 2601, 72, 40, 33)])
+@pytest.mark.parametrize("off", [0, 1, 2])
+def test_bases_on_any_boundary(lg, T, k, d, r, n, off):
+    """Given bases packed without padding (odd k: rows on 2-byte boundaries)
+    and starting inside an allocation: the bits of the padded ones."""
+    say(f"adapter bases at {off}: {T} {k} {d} {r} {n}")
+    c = case(T, k, d, r, n, False, torch.float32, "mixed", seed=off)
+    to = padded(torch.zeros(T, d, dtype=torch.bfloat16))
+    ref = apply(lg, c, out=to).contiguous().view(torch.int16).clone()
+    flat = torch.full((n * r * k + off,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    A = flat[off:].view(n, r, k)
+    A.copy_(c["A"])
+    to.zero_()
+    got = apply(lg, dict(c, A=A), out=to).contiguous().view(torch.int16)
+    assert torch.equal(got, ref)
+
+
 @pytest.mark.parametrize("signs", [True, False])
 def test_same_bits_again_and_inside_a_tile(lg, signs):
     """The same call twice, and rows that trade places inside their tiles of 32."""
