@@ -43,7 +43,10 @@ size_t logra_token_logprob_ws_bytes(int64_t n_tok, int64_t vocab, int32_t n_top)
  *   top_idx[t, i], top_logp[t, i], i < n_top: the tokens with the largest
  *     logits in descending order, equal logits in ascending order of their
  *     index, and their log probabilities.
- * One pass over the logits; sums are held in fp32 about a running maximum.
+ * One pass over the logits; sums are held in fp32 about a running maximum.  Logits
+ * may be of any finite size (masks of -1e30 or of the type's lowest value among
+ * them): values that z / tau takes past fp32's range count as infinitely far, and
+ * an lse or a log probability past it is infinite.
  *
  * Rows left out: a target outside [0, vocab) (e.g. -100 at a padded position)
  * marks a row whose logits are not read: logp, entropy and lse are 0,

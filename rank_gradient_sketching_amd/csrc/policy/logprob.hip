@@ -12,11 +12,13 @@
 // sum to more than 2^10.  d is one fused step, z l2t - mc with l2t = log2(e) /
 // tau and mc = m l2t rounded: that rounding is the same for every token of the
 // row, cancels in logp and H, and is added back in lse, so rows far from zero
-// keep their accuracy.  Where m l2t is past fp32's range (a row at the type's
-// lowest value) mc is infinite, the fused step fails for every group, and the
-// careful path takes the difference first.  That path also takes the groups with
-// a masked token (z = -inf: w = 0, d clamped at kLow in u, so that 0 * -inf does
-// not arise); NaN, and +inf, which becomes NaN, still reach s.
+// keep their accuracy.  It stays a small one (half a binade of a weight) only up to
+// |m l2t| = 2^24; past that (rows masked with -1e30, or at the type's lowest value)
+// mc is held as infinite, the fused step fails for every group, and the careful path
+// takes the difference z - m first, which is exact wherever its weight is not zero.
+// That path also takes the groups with a masked token (z = -inf: w = 0, d clamped
+// at kLow in u, so that 0 * -inf does not arise); NaN, and +inf, which becomes NaN,
+// still reach s.
 // The states of a wave meet in a butterfly and those of a row's waves in LDS,
 // always in the same order.
 // Alternatives.  Value and index of a token make one 64-bit key (the float's
@@ -56,34 +58,42 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLow = -1000.0f;   // 2^kLow is 0 in fp32
 constexpr float kMinFloat = -3.4028234663852886e38f;
+constexpr float kFusedEnd = 0x1p24f;   // half a step of fp32 below it is at most 1/2
 
 // ---------------------------------------------------------------- softmax states
 struct State {
   float m, s, u;
 };
 
-// d of logit z about the reference m: the fused step where m l2t is finite.
+// The rounded product m l2t of a reference that the fused step may be taken about;
+// infinite for others.
+__device__ __forceinline__ float centre(float m, float l2t) {
+  const float c = m * l2t;
+  return fabsf(c) < kFusedEnd ? c : INFINITY;
+}
+// d of logit z about the reference m, mc = centre(m, l2t).
 __device__ __forceinline__ float exponent(float z, float m, float mc, float l2t) {
   return isfinite(mc) ? fmaf(z, l2t, -mc) : (z - m) * l2t;
 }
-// The reference a as seen from the reference M >= a, clamped: a difference of the
-// rounded products that the weights were formed with (a fused one would not be).
-__device__ __forceinline__ float shift(float a, float M, float l2t) {
+// The reference a as seen from the reference M >= a, clamped (ca, cM: their
+// centres): a difference of what the weights were formed about, the rounded product
+// (so that nothing may be fused into it) or, past the fused step's end, the exact one.
+__device__ __forceinline__ float shift(float a, float ca, float M, float cM, float l2t) {
 #pragma clang fp contract(off)
-  const float ca = a * l2t, cM = M * l2t;
-  return fmaxf(isfinite(ca) && isfinite(cM) ? ca - cM : (a - M) * l2t, kLow);
+  float d = ca - cM;
+  if (__builtin_expect(!isfinite(d), 0))
+    d = isfinite(ca) ? fmaf(-M, l2t, ca) : isfinite(cM) ? fmaf(a, l2t, -cM) : (a - M) * l2t;
+  return fmaxf(d, kLow);
 }
 
 __device__ __forceinline__ State merge_states(const State& a, const State& b, float l2t) {
-  const float M = fmaxf(a.m, b.m);
-  const float da = shift(a.m, M, l2t);
-  const float db = shift(b.m, M, l2t);
-  const float fa = exp2_normal(da), fb = exp2_normal(db);
-  State o;
-  o.m = M;
-  o.s = fa * a.s + fb * b.s;
-  o.u = fa * fmaf(a.s, da, a.u) + fb * fmaf(b.s, db, b.u);
-  return o;
+  // about the larger reference, so that only the other one moves
+  const bool up = b.m > a.m;
+  const State hi{up ? b.m : a.m, up ? b.s : a.s, up ? b.u : a.u};
+  const State lo{up ? a.m : b.m, up ? a.s : b.s, up ? a.u : b.u};
+  const float d = shift(lo.m, centre(lo.m, l2t), hi.m, centre(hi.m, l2t), l2t);
+  const float f = exp2_normal(d);
+  return State{hi.m, fmaf(f, lo.s, hi.s), fmaf(f, fmaf(lo.s, d, lo.u), hi.u)};
 }
 
 __device__ __forceinline__ State wave_state(State st, float l2t) {
@@ -98,7 +108,7 @@ __device__ __forceinline__ State wave_state(State st, float l2t) {
   return st;
 }
 
-// Adds G elements; mc = st.m l2t goes along.
+// Adds G elements; mc = centre(st.m, l2t) goes along.
 template <int G>
 __device__ __forceinline__ void add_group(State& st, float& mc, const float* z, float l2t) {
   float gs, gu;
@@ -117,12 +127,13 @@ __device__ __forceinline__ void add_group(State& st, float& mc, const float* z, 
 #pragma unroll
     for (int e = 1; e < G; ++e) gmax = fmaxf(gmax, z[e]);
     if (gmax > st.m) {
-      const float dm = shift(st.m, gmax, l2t);
+      const float c = centre(gmax, l2t);
+      const float dm = shift(st.m, mc, gmax, c, l2t);
       const float f = exp2_normal(dm);
       st.u = f * fmaf(st.s, dm, st.u);
       st.s *= f;
       st.m = gmax;
-      mc = gmax * l2t;
+      mc = c;
     }
     gs = gu = 0.0f;
 #pragma unroll
@@ -442,14 +453,14 @@ __device__ __forceinline__ bool left_out(const LogprobArgs& a, int64_t row) {
 // log p of logit z in a row with state st.  (In units of log2 a logit at the
 // type's lowest value would overflow.)
 __device__ __forceinline__ float log_p(float z, const State& st, float l2t, float tau) {
-  const float d = kLn2 * exponent(z, st.m, st.m * l2t, l2t);
+  const float d = kLn2 * exponent(z, st.m, centre(st.m, l2t), l2t);
   return (isfinite(d) ? d : (z - st.m) / tau) - logf(st.s);
 }
 // By one thread of the row.
 __device__ __forceinline__ void write_row(const LogprobArgs& a, int64_t row, const State& st,
                                           float l2t, float zt) {
   const float ln_s = logf(st.s);
-  const float mc = st.m * l2t;
+  const float mc = centre(st.m, l2t);
   if (a.lse) {
     // (the weights are off by the rounding of mc, all alike)
     const float off = isfinite(mc) ? kLn2 * fmaf(st.m, l2t, -mc) : 0.0f;
@@ -510,7 +521,7 @@ __global__ __launch_bounds__(kThreads) void logprob_rows_kernel(LogprobArgs a, i
     const int64_t c0 = sp * piece;
     const int64_t c1 = c0 + piece < a.vocab ? c0 + piece : a.vocab;
     State st{kMinFloat, 0.0f, 0.0f};
-    float mc = st.m * l2t;
+    float mc = centre(st.m, l2t);
     BestKeys bk = no_keys(wbuf + (TOP ? wave * kBuf : 0));
     bool first = true;
     auto add = [&](const float* v, int64_t c) {

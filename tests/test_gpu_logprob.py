@@ -331,3 +331,79 @@ def test_refusals(lg):
     with pytest.raises(lg._lib.LograError):
         lg.token_logprob(padded(logits(4, 9000, "bf16", 1)), t, n_top=8,
                          ws=torch.zeros(256, device="cuda", dtype=torch.uint8))
+
+
+# ------------------------------------------------------------------ far logits
+def in_fp32(x):
+    """A reference value as fp32 holds it (past the range: infinite)."""
+    with np.errstate(over="ignore", invalid="ignore"):
+        return np.asarray(x, np.float64).astype(np.float32).astype(np.float64)
+
+
+def check_far(lg, z, t, tau, n_top):
+    """check_forward for logits of any finite size: log p of a far token is
+    ((z - m) l2t) ln 2 - ln s, six roundings of its magnitude (the difference, l2t,
+    two products, ln 2, the sum), and the reference is rounded to fp32, half a step
+    more; results past fp32's range are infinities."""
+    tau = float(np.float32(tau))
+    out = lg.token_logprob(z, t, tau=tau, n_top=n_top)
+    V = z.shape[1]
+    ref = olp.rows(f64(z), t.cpu().numpy(), tau, n_top)
+    R = U * (-(-V // 256) + 160)
+    lnV = np.log(V) + 1
+    size = lambda x: np.where(np.isfinite(x), np.abs(x), 0.0)
+    want = {k: in_fp32(ref[k]) for k in ("lse", "entropy", "logp", "top_logp")}
+    close(out.lse, want["lse"], R + 4 * U * size(want["lse"]), "lse")
+    close(out.entropy, want["entropy"], R * (2 + 2 * lnV), "entropy")
+    close(out.logp, want["logp"], R + 8 * U * (size(want["logp"]) + lnV), "logp")
+    if n_top:
+        assert np.array_equal(out.top_idx.cpu().numpy(), ref["top_idx"])
+        close(out.top_logp, want["top_logp"], R + 8 * U * (size(want["top_logp"]) + lnV), "top_logp")
+
+
+@pytest.mark.parametrize("tau", [0.7, 1.0, 1.5, 2.0])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,V", [(24, 9001), (24, 40000), (600, 2600)])
+def test_far_values(lg, n, V, dtype, tau):
+    """Finite values so large that one step of fp32 at z log2(e) / tau is more than
+    the exponent's whole range: as masks over the head, the tail, or all but a few
+    tokens of a row, in all of it, and as peaks above it.  (24 rows are cut into
+    pieces whose states are joined, 600 are not.)"""
+    say("logprob far", n, V, dtype, tau)
+    z = logits(n, V, dtype, 21)
+    t = torch.arange(n) * 37 % V
+    row = 0
+    for size in (1e8, 1e10, 1e20, 1e30, torch.finfo(z.dtype).max):
+        z[row] = -size                          # uniform: log p = -log V
+        z[row + 1, V // 3:] = -size             # the tail of the vocabulary
+        z[row + 2, :V - 700] = -size            # its head (the first groups of every thread)
+        z[row + 3, 1000:] = size                # a uniform distribution above a finite rest
+        t[row:row + 4] = torch.tensor([3, V - 1, V - 5, 17])
+        row += 4
+    z[row, ::2] = -torch.finfo(z.dtype).max     # every group holds some
+    z[row + 1] = torch.finfo(z.dtype).max
+    z[row + 2] = torch.linspace(-1e9, 1e9, V)   # one token far above the next
+    z[row + 3] = torch.linspace(1e9, -1e9, V)
+    check_far(lg, padded(z), t.cuda(), tau, 4)
+
+
+@pytest.mark.parametrize("tau", [0.7, 1.0, 1.5])
+@pytest.mark.parametrize("n,V", [(6, 9001), (600, 2600)])
+def test_where_the_fused_exponent_ends(lg, n, V, tau):
+    """fp32 rows whose values lie on both sides of |z| log2(e) / tau = 2^24, whole
+    numbers apart, so that threads whose references lie on either side are joined."""
+    say("logprob fused border", n, V, tau)
+    z = logits(n, V, "fp32", 22)
+    at = float(np.float32(2.0 ** 24 / np.log2(np.e) * tau))
+    rng = np.random.default_rng(23)
+    for row, sign in ((0, 1), (1, -1), (2, 1), (3, -1)):
+        step = torch.from_numpy(rng.integers(-3, 4, V).astype(np.float32))
+        z[row] = sign * round(at) + step
+        if row >= 2:                            # rising: every group raises its reference
+            z[row] = sign * round(at) + torch.arange(V, dtype=torch.float32) // (V // 16) - 8
+    z[4, :V // 2] = round(at) - 12
+    z[4, V // 2:] = round(at) + 12
+    z[5] = -round(at)
+    z[5, V - 1] = 1e7
+    t = torch.arange(n) * 37 % V
+    check_far(lg, padded(z), t.cuda(), tau, 0 if n > 100 else 4)
