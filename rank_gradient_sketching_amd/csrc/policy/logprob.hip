@@ -713,7 +713,8 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
     const float gh = a.d_entropy ? a.d_entropy[row] : 0.0f;
     const float H = a.d_entropy ? a.entropy[row] : 0.0f;
     // dz_j = p_j (k0 + k1 log p_j) + [j = target] kt
-    const float k0 = (gl - g - gh * H) * ih, k1 = -gh * ih, kt = g * ih;
+    // (lse - lse: NaN where it is not finite, and so in all of the row)
+    const float k0 = (gl - g - gh * H) * ih + (lse - lse), k1 = -gh * ih, kt = g * ih;
     auto gradient = [&](float* v, int64_t c) {
 #pragma unroll
       for (int e = 0; e < G; ++e) {

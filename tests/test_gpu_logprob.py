@@ -407,3 +407,28 @@ def test_where_the_fused_exponent_ends(lg, n, V, tau):
     z[5, V - 1] = 1e7
     t = torch.arange(n) * 37 % V
     check_far(lg, padded(z), t.cuda(), tau, 0 if n > 100 else 4)
+
+
+def test_gradient_rows_without_a_finite_lse(lg):
+    """Where z / tau leaves fp32's range the forward's lse is infinite: such a row's
+    gradient is NaN, whatever the signs, and its neighbours' are their own."""
+    say("logprob grad infinite lse")
+    n, V = 6, 3001
+    for dtype in ("bf16", "fp32"):
+        z = logits(n, V, dtype, 24)
+        z[1, 9] = 1e38
+        z[3] = -float("inf")
+        z[4] = -3e38
+        z = padded(z)
+        t = torch.tensor([5, 9, 6, 7, 8, -1]).cuda()
+        f = lg.token_logprob(z, t, tau=0.1)
+        assert f.lse[1] == float("inf") and f.lse[3] == f.lse[4] == -float("inf")
+        g, gh = torch.full((n,), 0.5, device="cuda"), torch.full((n,), -0.25, device="cuda")
+        H = torch.nan_to_num(f.entropy)         # (NaN itself would do)
+        for a, b, c in ((g, None, None), (None, gh, None), (None, None, g), (g, gh, g)):
+            dz = lg.token_logprob_backward(z, t, f.lse, None if b is None else H, a, b, c, tau=0.1)
+            assert torch.isnan(dz[[1, 3, 4]]).all(), dtype
+            assert torch.isfinite(dz[[0, 2, 5]]).all() and dz[5].eq(0).all()
+        lse = f.lse.clone()                     # (a left-out row stays zero)
+        lse[5] = float("inf")
+        assert lg.token_logprob_backward(z, t, lse, d_lse=g, tau=0.1)[5].eq(0).all()
