@@ -84,8 +84,8 @@ int logra_token_logprob(const void* z, int dtype, int64_t n_tok, int64_t vocab, 
  *           + d_lse p_j) / tau,    log p_j = z_j / tau - lse
  * computed in fp32 and rounded once to dtype (bf16: to nearest even).
  * Rows left out (a target outside [0, vocab)) get zeros.  Masked tokens
- * (z = -inf) get zero, but for the d_logp of a masked target.  Rows whose lse
- * is not finite give NaN.
+ * (z = -inf, or so low that z / tau is) get zero, but for the d_logp of a masked
+ * target.  Rows whose lse is not finite give NaN.
  *
  * z, dtype, n_tok, vocab, ld, target, tau: as in logra_token_logprob.
  * lse: device float[n_tok] of the forward call; entropy: likewise, needed only

@@ -700,6 +700,9 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
   // result has no use for it)
   const float ih = 1.0f / a.tau;
   const float il = fmaf(-a.tau, ih, 1.0f) / a.tau;
+  // (below this z / tau is past fp32's range and il's part does not matter, but
+  // would overflow by itself)
+  const float z_low = kMinFloat * fminf(a.tau, 1.0f);
   for (int64_t task = blockIdx.x; task < n_tasks; task += gridDim.x) {
     const int64_t row = task / n_pieces;
     const int64_t c0 = (task - row * n_pieces) * grad_cols(sizeof(T)) + wave * kWaveCols;
@@ -719,7 +722,7 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
 #pragma unroll
       for (int e = 0; e < G; ++e) {
         // (a masked token: p = 0, and log p kept finite)
-        const float low = sizeof(T) == 4 ? fmaf(fmaxf(v[e], kMinFloat), il, -lse) : -lse;
+        const float low = sizeof(T) == 4 ? fmaf(fmaxf(v[e], z_low), il, -lse) : -lse;
         const float lp = fmaf(v[e], ih, low);
         const float p = exp2_normal(lp * kLog2e);
         v[e] = p * fmaf(k1, fmaxf(lp, kLow), k0);

@@ -432,3 +432,33 @@ def test_gradient_rows_without_a_finite_lse(lg):
         lse = f.lse.clone()                     # (a left-out row stays zero)
         lse[5] = float("inf")
         assert lg.token_logprob_backward(z, t, lse, d_lse=g, tau=0.1)[5].eq(0).all()
+
+
+@pytest.mark.parametrize("tau", [4e-8, 3e-8, 1.7e-8, 1e-8, 7e-12, 1.3e-20])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gradient_masks_at_small_temperatures(lg, dtype, tau):
+    """Masked tokens, by -inf and by the type's lowest value, are zero at any
+    temperature; the others follow the formula."""
+    say("logprob grad small tau", dtype, tau)
+    n, V, tau = 4, 2050, float(np.float32(tau))
+    z = (logits(n, V, "fp32", 25).double() * tau).to(DT[dtype])
+    z[0, 100:] = -float("inf")
+    z[1, ::3] = torch.finfo(z.dtype).min
+    z[2, :600] = -1e30
+    z = padded(z)
+    t = torch.tensor([200, 1, 700, 5]).cuda()   # (row 0: a masked one is given)
+    f = lg.token_logprob(z, t, tau=tau)
+    g, gh = torch.full((n,), 0.5, device="cuda"), torch.full((n,), -0.25, device="cuda")
+    dz = lg.token_logprob_backward(z, t, f.lse, f.entropy, g, gh, tau=tau)
+    assert dz[0, 100:200].eq(0).all() and dz[0, 201:].eq(0).all()
+    assert abs(dz[0, 200].item() * tau - 0.5) <= 0.5 * 2.0 ** -7
+    assert dz[1, ::3].eq(0).all() and dz[2, :600].eq(0).all()
+    zz, ok = f64(z), np.arange(1, n)
+    ref = olp.gradient(zz, t.cpu().numpy(), tau, f64(f.lse), f64(f.entropy), f64(g), f64(gh))[ok]
+    # (log p's error u (|lse| + |log p|) + 2 u |log p|, beside a factor of up to
+    # 0.5 + 0.25 (H + |log p|) <= 8; H <= ln V = 8, |log p| <= 25)
+    with np.errstate(over="ignore"):
+        p = np.exp(zz / tau - f64(f.lse)[:, None])[ok]
+    step = 2.0 ** -8 if dtype == "bf16" else U
+    tol = U * (100 * p * 8 + 2) / tau + step * np.abs(ref)
+    assert np.all(np.abs(f64(dz)[ok] - ref) <= tol), np.max(np.abs(f64(dz)[ok] - ref) / tol)
