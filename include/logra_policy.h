@@ -85,7 +85,9 @@ int logra_token_logprob(const void* z, int dtype, int64_t n_tok, int64_t vocab, 
  * computed in fp32 and rounded once to dtype (bf16: to nearest even).
  * Rows left out (a target outside [0, vocab)) get zeros.  Masked tokens
  * (z = -inf, or so low that z / tau is) get zero, but for the d_logp of a masked
- * target.  Rows whose lse is not finite give NaN.
+ * target.  Rows whose lse is not finite give NaN.  The factors d_logp / tau, d_lse /
+ * tau and d_entropy (entropy + 128) / tau have to lie inside fp32's range: past it a
+ * row holds infinities and NaN.
  *
  * z, dtype, n_tok, vocab, ld, target, tau: as in logra_token_logprob.
  * lse: device float[n_tok] of the forward call; entropy: likewise, needed only

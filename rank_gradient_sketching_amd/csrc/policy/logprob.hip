@@ -57,6 +57,7 @@ constexpr int kWaves = kThreads / 64;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLow = -1000.0f;   // 2^kLow is 0 in fp32
+constexpr float kLowLn = -128.0f;  // and so is e^kLowLn
 constexpr float kMinFloat = -3.4028234663852886e38f;
 constexpr float kFusedEnd = 0x1p24f;   // half a step of fp32 below it is at most 1/2
 
@@ -725,7 +726,7 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
         const float low = sizeof(T) == 4 ? fmaf(fmaxf(v[e], z_low), il, -lse) : -lse;
         const float lp = fmaf(v[e], ih, low);
         const float p = exp2_normal(lp * kLog2e);
-        v[e] = p * fmaf(k1, fmaxf(lp, kLow), k0);
+        v[e] = p * fmaf(k1, fmaxf(lp, kLowLn), k0);
       }
       if (target >= c && target < c + kWaveCols) {
 #pragma unroll

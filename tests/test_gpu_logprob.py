@@ -462,3 +462,10 @@ def test_gradient_masks_at_small_temperatures(lg, dtype, tau):
     step = 2.0 ** -8 if dtype == "bf16" else U
     tol = U * (100 * p * 8 + 2) / tau + step * np.abs(ref)
     assert np.all(np.abs(f64(dz)[ok] - ref) <= tol), np.max(np.abs(f64(dz)[ok] - ref) / tol)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gradient_masks_at_the_smallest_temperatures(lg, dtype):
+    """1 / tau near fp32's largest value: a masked token's clamped log p must not
+    carry the entropy's factor past it."""
+    test_gradient_masks_at_small_temperatures(lg, dtype, 2e-37)
