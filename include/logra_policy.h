@@ -82,7 +82,10 @@ int logra_token_logprob(const void* z, int dtype, int64_t n_tok, int64_t vocab, 
  * lse down to the logits:
  *   dz_j = (d_logp ([j = target] - p_j) - d_entropy p_j (log p_j + entropy)
  *           + d_lse p_j) / tau,    log p_j = z_j / tau - lse
- * computed in fp32 and rounded once to dtype (bf16: to nearest even).
+ * computed in fp32 and rounded once to dtype (bf16: to nearest even).  log p_j
+ * carries the rounding of lse (2^-24 of it) and is held to at most 0: in rows so far
+ * from zero that lse resolves whole units only, p_j is off by such a factor but stays
+ * in [0, 1].
  * Rows left out (a target outside [0, vocab)) get zeros.  Masked tokens
  * (z = -inf, or so low that z / tau is) get zero, but for the d_logp of a masked
  * target.  Rows whose lse is not finite give NaN.  The factors d_logp / tau, d_lse /

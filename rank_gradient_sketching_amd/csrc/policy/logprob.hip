@@ -724,7 +724,9 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
       for (int e = 0; e < G; ++e) {
         // (a masked token: p = 0, and log p kept finite)
         const float low = sizeof(T) == 4 ? fmaf(fmaxf(v[e], z_low), il, -lse) : -lse;
-        const float lp = fmaf(v[e], ih, low);
+        // (the rounding of a large lse must not carry p past 1; NaN stays)
+        const float x = fmaf(v[e], ih, low);
+        const float lp = x > 0.0f ? 0.0f : x;
         const float p = exp2_normal(lp * kLog2e);
         v[e] = p * fmaf(k1, fmaxf(lp, kLowLn), k0);
       }

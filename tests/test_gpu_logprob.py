@@ -469,3 +469,35 @@ def test_gradient_masks_at_the_smallest_temperatures(lg, dtype):
     """1 / tau near fp32's largest value: a masked token's clamped log p must not
     carry the entropy's factor past it."""
     test_gradient_masks_at_small_temperatures(lg, dtype, 2e-37)
+
+
+@pytest.mark.parametrize("tau", [0.7, 1.0, 1.5])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_gradient_of_far_rows(lg, dtype, tau):
+    """Rows that are masked whole by a large finite value, or peak at one: fp32's lse
+    cannot tell their tokens apart, but no p is above 1, so the gradient stays finite,
+    and zero where the loss's own gradients are.  Rows with a part masked follow the
+    formula."""
+    say("logprob grad far rows", dtype, tau)
+    n, V, tau = 18, 3001, float(np.float32(tau))
+    z = logits(n, V, dtype, 26)
+    sizes = (1e6, 3e7, 1e10, 7e15, 1e20, 1e30)
+    for i, size in enumerate(sizes):
+        z[3 * i] = -size
+        z[3 * i + 1, V // 2:] = size
+        z[3 * i + 2, V // 2:] = -size
+    z = padded(z)
+    t = (torch.arange(n) * 37 % (V // 2)).cuda()
+    f = lg.token_logprob(z, t, tau=tau)
+    g, gh = torch.full((n,), 0.5, device="cuda"), torch.full((n,), -0.25, device="cuda")
+    dz = lg.token_logprob_backward(z, t, f.lse, f.entropy, g, gh, tau=tau)
+    # (0.5 + 0.25 (H + 0) with p = 1, or e^-1 / 4 more; and the target's 0.5)
+    assert torch.isfinite(dz).all() and dz.float().abs().max().item() <= (1 + 0.25 * 9) / tau
+    part = torch.arange(2, n, 3).cuda()
+    sel = lambda x: x[part].contiguous()
+    check_grad(z[part], t[part], tau, sel(f.lse), sel(f.entropy), sel(g), sel(gh), None, dz[part])
+    zero = torch.zeros(n, device="cuda")
+    assert lg.token_logprob_backward(z, t, f.lse, f.entropy, zero, zero, tau=tau).eq(0).all()
+    # a NaN logit beside a finite lse is still seen
+    z[2, 5] = float("nan")
+    assert torch.isnan(lg.token_logprob_backward(z, t, f.lse, d_logp=g, tau=tau)[2, 5])
