@@ -80,7 +80,8 @@ __device__ __forceinline__ uint32_t encode(const float* x, uint32_t h0, bool lea
   int top = 0;
 #pragma unroll
   for (int e = 0; e < kVec; ++e) {
-    t[e] = __float_as_uint(x[e]) + ((h0 + (uint32_t)e * kDitherIndex) >> (9 + KEEP));
+    // (without a NaN's sign, which the dither would carry out of the word)
+    t[e] = __float_as_uint(fabsf(x[e])) + ((h0 + (uint32_t)e * kDitherIndex) >> (9 + KEEP));
     top = max(top, (int)(t[e] >> 23));
   }
   const int E = min(max(block_max(top), kExpMin), kExpNan);

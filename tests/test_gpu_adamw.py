@@ -350,3 +350,31 @@ def test_state_values_of_every_code(lg, which, off):
     want = oad.decode(codes[:n], exps, which)
     assert np.array_equal(f64(out), want, equal_nan=True)
     assert np.isnan(want[-251:]).all() and np.isfinite(want[:-251]).all()
+
+
+@pytest.mark.parametrize("grad", ["bf16", "fp32"])
+def test_nan_gradients_of_every_payload(lg, grad):
+    """8-bit states: a NaN marks both states' blocks whatever its sign and its
+    payload (all bits set, e.g. of memory filled with 0xFF), under any dither;
+    every other block is what it is without."""
+    say("adamw nan payloads", grad)
+    bits = ([0x7FFF, 0xFFFF, 0xFFFE, 0x7F81, 0xFF81, 0xFFC0] if grad == "bf16" else
+            [0x7FFFFFFF, 0xFFFFFFFF, 0xFFFFFFFE, 0xFFF80000, 0xFFF7FFFF, 0x7F800001, 0xFF800001,
+             0xFFC00000])
+    whole = torch.int16 if grad == "bf16" else torch.int32
+    wrap = 1 << (16 if grad == "bf16" else 32)
+    n = 64 * len(bits)
+    for step in (3, 4, 5, 6):
+        clean, q = (tensors([n], "bf16", grad, True, 8, 0, 9)[0] for _ in range(2))
+        for i, b in enumerate(bits):
+            at = 64 * i + (7 * i + step) % 32           # every other block of 32
+            q["g"].view(whole)[at] = b - wrap if b >= wrap // 2 else b
+        for x in (clean, q):
+            lg.adamw_step(bind(lg, [x], 0.1), LR, step)
+        for which in ("m", "v"):
+            e = q[which + "_exp"].cpu()
+            assert e[::2].eq(255).all(), (which, step, e[::2])
+            assert torch.equal(e[1::2], clean[which + "_exp"].cpu()[1::2])
+            got = lg.adamw_state_values(q[which], q[which + "_exp"], which).view(-1, 2, 32)
+            ref = lg.adamw_state_values(clean[which], clean[which + "_exp"], which).view(-1, 2, 32)
+            assert torch.isnan(got[:, 0]).all() and torch.equal(got[:, 1], ref[:, 1])
