@@ -121,7 +121,7 @@ __global__ __launch_bounds__(64 * proj_waves(NB)) void adapter_project_kernel(
   const int split = rest % n_split;
   const int deal = rest / n_split;
   const int64_t t0 = (int64_t)tile * kTileRows;
-  const int all_chunks = (a.k + kChunk - 1) / kChunk;
+  const int all_chunks = (a.k - 1) / kChunk + 1;   // (k may end at 2^31 - 1)
   const int ch0 = split * chunks_per_split;
   const int n_chunks = min(chunks_per_split, all_chunks - ch0);
   // work-groups start at different chunks: in step they would all read the same
@@ -209,7 +209,7 @@ __global__ __launch_bounds__(64 * proj_waves(NB)) void adapter_project_kernel(
   };
   auto compute = [&](int id, const Signs& sw, uint32_t keep, int c, int hc,
                      const unsigned char* buf) LOGRA_INLINE {
-    if ((c + 1) * kChunk > a.k)     // the chunk that ends past k
+    if (c * kChunk > a.k - kChunk)  // the chunk that ends past k
       compute_cols(std::true_type{}, id, sw, keep, c, hc, buf);
     else
       compute_cols(std::false_type{}, id, sw, keep, c, hc, buf);

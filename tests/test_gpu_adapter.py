@@ -272,3 +272,42 @@ def test_refusals(lg):
         call(ws=torch.zeros(64, dtype=torch.uint8, device="cuda"))
     with pytest.raises(lg._lib.LograError):
         call(out=c["X"])                              # out over X
+
+
+@pytest.mark.parametrize("basis", ["signs", "rows", "any rows"])
+@pytest.mark.parametrize("k", [2 ** 31 - 1, 2 ** 31 - 255])
+def test_the_longest_rows(lg, k, basis):
+    """k up to the last one accepted, where the chunk count and a column past the
+    last chunk pass 31 bits.  X is zero but for some columns, so the oracle needs
+    only those of A; X and A end in NaN padding where their rows have any."""
+    say("adapter longest rows", k, basis)
+    from oracle.philox import philox4x64_10_np
+    T, d, r, seed = 2, 24, 2, 91
+    cols = np.array([0, 1, 255, 256, 2 ** 30 + 3, k - 600, k - 257, k - 256, k - 200, k - 9, k - 2, k - 1])
+    at = torch.from_numpy(cols).cuda()
+    X = torch.zeros(T, 2 ** 31, dtype=torch.bfloat16, device="cuda")
+    X[:, k:] = float("nan")
+    X[:, at] = normal((T, len(cols)), 1).cuda()
+    U, Y = normal((1, d, r), 3, 15.0, torch.float32).cuda(), padded(normal((T, d), 2))
+    args = {}
+    if basis == "signs":
+        j = cols.astype(np.uint64)
+        words = np.stack(philox4x64_10_np((j >> np.uint64(8))[None], np.arange(r, dtype=np.uint64)[:, None],
+                                          np.uint64(0), np.uint64(0), seed, 0), axis=-1)
+        word = np.take_along_axis(words, ((cols >> 6) & 3)[None, :, None], axis=2)[:, :, 0]
+        A = (1.0 - 2.0 * ((word >> (j & np.uint64(63))[None]) & np.uint64(1)).astype(np.float64)) / np.sqrt(r)
+        args["seeds"] = torch.tensor([[seed, 0]], device="cuda")
+    else:
+        # (rows k apart start on any boundary)
+        full = torch.zeros(r * (k if basis == "any rows" else 2 ** 31), dtype=torch.bfloat16,
+                           device="cuda").view(1, r, -1)
+        full[:, :, k:] = float("nan")
+        full[0, :, at] = normal((r, len(cols)), 4).cuda()
+        A, args["A"] = f64(full[0, :, at]), full[:, :, :k]
+    ids = torch.zeros(T, dtype=torch.int32, device="cuda")
+    out = lg.adapter_apply(X[:, :k], Y, ids, U, torch.ones(1, device="cuda"),
+                           out=padded(torch.zeros(T, d, dtype=torch.bfloat16)), **args)
+    ref, M = oad.apply(f64(X[:, at]), f64(Y), np.zeros(T, int), f64(U), [A], np.ones(1))
+    tol = 2.0 ** -8 * np.abs(ref) + M * ((len(cols) + 3 * r + 64) * 2.0 ** -24 + 3 * 2.0 ** -16)
+    assert np.all(np.abs(f64(out) - ref) <= tol)
+    assert np.abs(ref - f64(Y)).max() > 1                 # (an update that is seen)
