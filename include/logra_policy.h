@@ -182,8 +182,8 @@ int logra_adamw_table(int32_t n, const logra_adamw_item* items, void* table, siz
  *
  * table: host memory as logra_adamw_table left it; table_dev: device copy of the
  *     same bytes, 8-B aligned (not inspected when there is nothing to do).
- * lr, beta1, beta2, eps finite; beta in [0, 1) as a float; lr, eps >= 0 (with eps 0 an
- *     entry whose v is zero becomes NaN); step >= 1.
+ * lr, eps finite as floats and >= 0 (with eps 0, also as a float, an entry whose v is
+ *     zero becomes NaN); beta1, beta2 in [0, 1) as floats; step >= 1.
  * Returns LOGRA_OK, LOGRA_EINVAL or LOGRA_EHIP.
  */
 int logra_adamw_step(const void* table, const void* table_dev, double lr, double beta1,

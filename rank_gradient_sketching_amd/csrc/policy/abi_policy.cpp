@@ -208,7 +208,8 @@ int logra_adamw_step(const void* table, const void* table_dev, double lr, double
   if (table == nullptr || !aligned(table, 8)) return LOGRA_EINVAL;
   const logra::AdamwTable& t = *static_cast<const logra::AdamwTable*>(table);
   if (t.magic != kTableMagic) return LOGRA_EINVAL;
-  if (!isfinite(lr) || lr < 0.0 || !isfinite(eps) || eps < 0.0 || step < 1) return LOGRA_EINVAL;
+  if (!isfinite((float)lr) || lr < 0.0 || !isfinite((float)eps) || eps < 0.0 || step < 1)
+    return LOGRA_EINVAL;
   for (const double b : {beta1, beta2})
     if (!isfinite(b) || b < 0.0 || !((float)b < 1.0f)) return LOGRA_EINVAL;
   if (!aligned(grad_scale, 4)) return LOGRA_EINVAL;

@@ -162,6 +162,15 @@ def test_adamw_step_rejects(L, kw):
     assert _step(L, ctypes.addressof(buf), **kw) == EINVAL
 
 
+@pytest.mark.parametrize("kw", [dict(lr=1e39), dict(eps=1e39), dict(lr=-1e-300), dict(b1=-1e-300)])
+def test_adamw_step_rejects_scalars_past_fp32(L, kw):
+    """The kernels take fp32 scalars: an lr that is infinite there would turn entries
+    without a step into NaN."""
+    st, buf = _table(L)
+    assert st == OK
+    assert _step(L, ctypes.addressof(buf), **kw) == EINVAL
+
+
 def test_adamw_step_needs_a_table_and_work(L):
     assert _step(L, None) == EINVAL
     buf = (ctypes.c_uint64 * 256)()
