@@ -247,6 +247,8 @@ def adamw_bind(params, grads, m, v, master=None, m_exp=None, v_exp=None, weight_
     exps = columns[5][1], columns[6][1]
     for i in range(n):
         p = params[i]
+        if not isinstance(p, torch.Tensor):
+            raise TypeError(f"p[{i}] must be a torch.Tensor")
         if dev is None:
             _need(p, "p[0]", _EITHER)
             dev = p.get_device()

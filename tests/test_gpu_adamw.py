@@ -378,3 +378,16 @@ def test_nan_gradients_of_every_payload(lg, grad):
             got = lg.adamw_state_values(q[which], q[which + "_exp"], which).view(-1, 2, 32)
             ref = lg.adamw_state_values(clean[which], clean[which + "_exp"], which).view(-1, 2, 32)
             assert torch.isnan(got[:, 0]).all() and torch.equal(got[:, 1], ref[:, 1])
+
+
+def test_bind_names_what_is_no_tensor(lg):
+    say("adamw bind types")
+    t = lambda: torch.zeros(64, device="cuda")
+    four = [[t(), t()] for _ in range(4)]
+    for i, name in enumerate("pgmv"):
+        args = [list(x) for x in four]
+        args[i][1] = 3.0
+        with pytest.raises(TypeError, match=rf"{name}\[1\] must be a torch.Tensor"):
+            lg.adamw_bind(*args)
+    with pytest.raises(TypeError, match=r"p\[1\] must be a torch.Tensor"):
+        lg.adamw_bind([t(), None], *four[1:])
