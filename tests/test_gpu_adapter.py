@@ -311,3 +311,82 @@ def test_the_longest_rows(lg, k, basis):
     tol = 2.0 ** -8 * np.abs(ref) + M * ((len(cols) + 3 * r + 64) * 2.0 ** -24 + 3 * 2.0 ** -16)
     assert np.all(np.abs(f64(out) - ref) <= tol)
     assert np.abs(ref - f64(Y)).max() > 1                 # (an update that is seen)
+
+
+# The kernels of many rows: from 8192 blocks of 16 rows x 64 columns on, those of
+# rank up to 64 whose rows of U lie on 16-byte boundaries by adapter_rows_kernel,
+# others by adapter_strip_kernel.  k of 2600 and more is cut into pieces.
+MANY = [
+    # kernel, T, k, d, r, n, rows, U's type, entries U lies off a boundary
+    ("rows", 8201, 136, 1100, 8, 5, "runs", "bf16", 0),
+    ("rows", 8201, 264, 1100, 64, 5, "mixed", "fp32", 0),
+    ("rows", 2500, 2600, 3400, 32, 3, "mixed", "bf16", 0),
+    ("rows", 2500, 2600, 3400, 40, 8, "runs", "fp32", 0),
+    ("rows", 600, 5000, 17000, 64, 6, "runs", "bf16", 0),
+    ("rows", 9000, 300, 1031, 16, 1, "one", "fp32", 0),
+    ("rows", 33000, 136, 260, 4, 40, "mixed", "fp32", 0),
+    ("rows", 16500, 136, 515, 64, 300, "runs", "fp32", 0),
+    ("strip", 8201, 136, 1100, 24, 5, "mixed", "bf16", 3),
+    ("strip", 8201, 264, 1100, 64, 5, "runs", "fp32", 1),
+    ("strip", 2500, 2600, 3400, 100, 8, "runs", "bf16", 0),
+    ("strip", 2500, 2600, 3400, 100, 3, "mixed", "fp32", 0),
+    ("strip", 600, 5000, 17000, 256, 6, "runs", "fp32", 0),
+    ("strip", 9000, 300, 1031, 128, 1, "one", "bf16", 0),
+    ("strip", 8201, 136, 1100, 128, 33, "mixed", "fp32", 0),
+    ("strip", 33000, 136, 260, 250, 12, "runs", "fp32", 0),
+    ("strip", 16500, 136, 515, 7, 40, "mixed", "fp32", 0),
+]
+
+
+@pytest.mark.parametrize("signs", [True, False])
+@pytest.mark.parametrize("kernel,T,k,d,r,n,rows,u_type,off", MANY)
+def test_many_rows(lg, kernel, T, k, d, r, n, rows, u_type, off, signs):
+    say("adapter many rows", kernel, T, k, d, r, n, rows, u_type, off, signs)
+    u_dtype = torch.float32 if u_type == "fp32" else torch.bfloat16
+    vec = r % (4 if u_type == "fp32" else 8) == 0 and off == 0
+    assert -(-T // 16) * -(-d // 64) >= 8192
+    assert kernel == ("rows" if vec and r <= 64 else "strip")
+    c = case(T, k, d, r, n, signs, u_dtype, rows)
+    if off:
+        U = torch.empty(c["U"].numel() + off, dtype=u_dtype, device="cuda")[off:].view_as(c["U"])
+        c["U"] = U.copy_(c["U"])
+    out = padded(torch.zeros(T, d, dtype=torch.bfloat16), 2)
+    pad = out._base[:, d:].clone().view(torch.int16)
+    apply(lg, c, out=out)
+    check(c, out)
+    bits = out.contiguous().view(torch.int16)
+    assert torch.equal(out._base[:, d:].clone().view(torch.int16), pad)
+    none = c["adapter"] < 0
+    assert torch.equal(bits[none], c["Y"].contiguous().view(torch.int16)[none])
+    # in place, the same bits
+    Y = padded(c["Y"].cpu(), 1)
+    same = lg.adapter_apply(c["X"], Y, c["adapter"], c["U"], c["scale"], seeds=c.get("seeds"),
+                            A=c.get("A"))
+    assert same is Y and torch.equal(Y.contiguous().view(torch.int16), bits)
+    assert Y._base[:, d:].isnan().all()
+
+
+@pytest.mark.parametrize("r", [32, 128])
+def test_many_rows_do_not_touch_each_other(lg, r):
+    """NaN and infinite rows, a NaN policy and indices out of range among many rows:
+    every other row is what it is without them."""
+    say("adapter many rows, isolation", r)
+    T, d = 8300, 1100
+    c = case(T, 264, d, r, 5, True, torch.float32, "mixed", seed=3)
+    to = padded(torch.zeros(T, d, dtype=torch.bfloat16))
+    ref = apply(lg, c, out=to).contiguous().view(torch.int16).clone()
+    bad = dict(c, X=padded(c["X"].cpu()), U=c["U"].clone(), adapter=c["adapter"].clone())
+    bad["X"][7::100] = float("nan")
+    bad["X"][20::100, 3] = float("inf")
+    bad["U"][2] = float("nan")
+    out_of = torch.arange(31, T, 100, device="cuda")
+    bad["adapter"][out_of] = torch.tensor([5, -2 ** 31, 2 ** 31 - 1, 77], dtype=torch.int32,
+                                          device="cuda").repeat(len(out_of))[:len(out_of)]
+    got = apply(lg, bad, out=to)
+    ok = (c["adapter"] != 2)
+    for first in (7, 20, 31):
+        ok[first::100] = False
+    bits = got.contiguous().view(torch.int16)
+    assert torch.equal(bits[ok], ref[ok])
+    assert torch.equal(bits[out_of], c["Y"].contiguous().view(torch.int16)[out_of])
+    assert torch.isnan(got[(c["adapter"] == 2) & (bad["adapter"] == 2)]).all()
