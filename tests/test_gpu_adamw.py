@@ -391,3 +391,68 @@ def test_bind_names_what_is_no_tensor(lg):
             lg.adamw_bind(*args)
     with pytest.raises(TypeError, match=r"p\[1\] must be a torch.Tensor"):
         lg.adamw_bind([t(), None], *four[1:])
+
+
+def layout(bound, form):
+    """(tensors, work-groups, steps of a work-group) of a form in a bound table:
+    five 32-bit numbers a form behind two 64-bit ones."""
+    return tuple(np.frombuffer(bound.table, np.int32)[4 + 5 * form:7 + 5 * form].tolist())
+
+
+# from this many entries in a form on, a work-group takes four steps of 1024 (about
+# 2^22 entries: 1024 work-groups)
+LONG = [1, 4300007, 33, 4095, 4097, 12345, 1023, 1025, 7]
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("form", range(6))
+def test_long_tensors(lg, form, bits):
+    """Work-groups of four steps: whole ones, ones that end inside each of their
+    steps, single entries; on vector boundaries and (every other form) off them."""
+    param, grad, master = FORMS[form]
+    off = (form + bits // 8) % 2
+    say("adamw long", param, grad, master, bits, off)
+    qs = tensors(LONG, param, grad, master, bits, off, 11)
+    weights = 0 if param == "fp32" else 2 if master else 1
+    table = layout(bind(lg, qs, 0.1), weights * 4 + (2 if grad == "fp32" else 0) + (bits == 8))
+    assert table == (len(LONG), sum(-(-n // 4096) for n in LONG), 4)
+    del qs
+    run_and_check(lg, LONG, param, grad, master, bits, off, [0.1, 0.0, 0.05] * 3, steps=(9,),
+                  gscale=0.7 if form == 2 else None, seed=11)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_long_and_short_work_groups_agree(lg, bits):
+    """A tensor steps to the same bits in a table of long work-groups and alone in
+    one of short ones (the dither counts the entries of the tensors before it)."""
+    say("adamw long and short", bits)
+    n = [50001, 4300800]
+    a = tensors(n, "bf16", "bf16", True, bits, 0, 12)
+    b = tensors(n, "bf16", "bf16", True, bits, 0, 12)[0]
+    both, one = bind(lg, a, 0.1), bind(lg, [b], 0.1)
+    assert layout(both, 8 + (bits == 8))[2] == 4 and layout(one, 8 + (bits == 8))[2] == 1
+    for step in (1, 2):
+        lg.adamw_step(both, LR, step)
+        lg.adamw_step(one, LR, step)
+    for k in ("p", "master", "m", "v", "m_exp", "v_exp"):
+        assert b[k] is None or torch.equal(a[0][k], b[k]), k
+
+
+def test_a_handle_steps_the_storage_it_was_bound_to(lg):
+    """What the binding promises: tensors given other storage later are not seen, the
+    old ones are kept and stepped; a new handle steps the new ones."""
+    say("adamw handle and storage")
+    t = lambda x: torch.full((70,), x, device="cuda")
+    p, g, m, v = t(1.0), t(2.0), t(0.0), t(0.0)
+    bound = lg.adamw_bind([p], [g], [m], [v])
+    old_p, old_g = p.detach(), g.detach()
+    p.data, g.data = t(5.0), t(-2.0)
+    lg.adamw_step(bound, 0.5, 1)
+    assert p.eq(5.0).all() and (old_p - 0.5).abs().max() < 1e-6
+    del old_g                                     # (the handle keeps it)
+    lg.adamw_step(bound, 0.5, 2)
+    assert p.eq(5.0).all() and old_p.abs().max() < 1e-6
+    m.zero_()
+    v.zero_()
+    lg.adamw_step(lg.adamw_bind([p], [g], [m], [v]), 0.5, 1)
+    assert (p - 5.5).abs().max() < 1e-6 and old_p.abs().max() < 1e-6
