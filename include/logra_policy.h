@@ -10,7 +10,8 @@
  * between calls, work enqueued on `stream`, every argument that the host can
  * see checked before any HIP call, no synchronisation.  None of the entry
  * points records a memset, so all of them can be captured in a HIP graph
- * (host scalars are then fixed at their values of the capture).
+ * (host scalars are then fixed at their values of the capture: what that means for
+ * an optimizer's step stands at logra_adamw_step).
  */
 #ifndef LOGRA_POLICY_H
 #define LOGRA_POLICY_H
@@ -179,6 +180,12 @@ int logra_adamw_table(int32_t n, const logra_adamw_item* items, void* table, siz
  *   average as they should; rounded to nearest, a v with beta2 = 0.999 stays
  *   where it is (0.1 % of a step against a spacing of 6 %).
  *   Zeroed codes with any E below 255 are the zero state.
+ *
+ * In a captured graph lr, step and with it the bias corrections and the dither keep
+ * the values of the capture at every replay.  Past the first steps, with the bias
+ * corrections near 1, fp32 states do not need them to move; 8-bit states do: under
+ * one and the same dither they are rounded with a bias, so this call stays outside
+ * a graph there (or in as many graphs as there are steps).
  *
  * table: host memory as logra_adamw_table left it; table_dev: device copy of the
  *     same bytes, 8-B aligned (not inspected when there is nothing to do).

@@ -21,12 +21,12 @@
 //
 // Bound: HBM bytes (a bf16 weight with fp32 master, bf16 gradient and fp32
 // states moves 28 bytes an entry, 8-bit states 16): 233 M entries in 1165 us (5.6
-// TB/s) and 690 us (5.4 TB/s).  A work-group takes 4096
-// consecutive entries of one tensor, every load of its four steps issued
-// before the first is used.  The tensors stand in a table in device memory,
-// where a work-group finds its own by comparing 64 tensors' first work-groups
-// at once, one per lane (a level more for every 64 times as many).  All tensors
-// of a form are one launch: 140 small ones take 4.0 us.
+// TB/s) and 713 us (5.3 TB/s).  A work-group takes 4096 consecutive entries of
+// one tensor, every load of its four steps issued before the first is used.  The
+// tensors stand in a table in device memory, where a work-group finds its own by
+// comparing 64 tensors' first work-groups at once, one per lane (a level more for
+// every 64 times as many).  All tensors of a form are one launch: 140 small ones
+// take 4.0 us.
 #include <math.h>
 
 #include <type_traits>
@@ -44,7 +44,7 @@ constexpr int kVec = 4;                              // entries per lane and ste
 constexpr int kStep = kThreads * kVec;               // entries per work-group and step
 constexpr int kManySteps = 4;
 // Below this many work-groups of kManySteps steps, one step each: 23 ragged tensors
-// of 640 k entries with 8-bit states took 11 us in 160 work-groups, 6.4 in steps of
+// of 640 k entries with 8-bit states took 11 us in 160 work-groups, 6.1 in steps of
 // their own (140 tensors of 1536 and 256 entries the same 4 us, latency).
 constexpr int64_t kFew = 1024;
 
@@ -303,7 +303,7 @@ __device__ __forceinline__ uint32_t value_pair(uint32_t w, uint32_t base) {
 
 // Eight entries per lane and step, four steps: 8-byte loads and 16-byte stores that
 // cover whole lines in every instruction (with 16 entries a lane, each store had
-// every other 16 bytes of its lines, 181 and 132 us).  233 M entries: 113 us, 6.2
+// every other 16 bytes of its lines, 181 and 132 us).  233 M entries: 116 us, 6.2
 // TB/s.
 constexpr int kValues = 8;
 constexpr int kValueSteps = 4;

@@ -68,16 +68,17 @@ struct Policies {
 // multiplied; 16-byte piece j of row t lies at slot j ^ (t % 16) against bank
 // conflicts.  In step s of a half, lanes 0-31 / 32-63 carry its columns 8 s ..
 // / 64 + 8 s ..: byte s of one of the sign block's four words.
-// 8192 x 4096 at rank 64: 19.5 us where every tile has one policy (3.4 TB/s; the
+// 8192 x 4096 at rank 64: 18.4 us where every tile has one policy (3.6 TB/s; the
 // vector unit, which expands the signs), 30 us with tiles of two among them, which
-// end last.  One token: 7.2 us, latency.
+// end last.  Given bases are read again by every tile: 97 us there.  One token: 7.2
+// us, latency.
 constexpr int kHalfCols = 128;
 constexpr int kHalfBytes = kTileRows * kHalfCols * 2;
 constexpr int kRedRow = 36;   // floats of a token's 32 partial sums in LDS
 constexpr int proj_waves(int nb) { return nb <= 4 ? 8 : 4; }
 
 // Where A comes from: its seed, or memory (rows on 16-byte boundaries, or on any:
-// 612 rows of 33 policies, r = 100, take 21 us with k = 1040 and 42 with 1041).
+// 612 mixed rows of 33 policies, r = 100, take 44 us with k = 1040 and 83 with 1041).
 enum class Basis { kSigns, kRows, kAnyRows };
 
 // Elements col .. col + 7 of a row that lies on any boundary; `edge`: ones past k
@@ -821,8 +822,8 @@ __global__ __launch_bounds__(256, 2) void adapter_rows_kernel(AdapterArgs a, int
 // time lie in LDS in operand order (converted once for the work-group's rows, 64
 // KB at r = 256 in fp32).  A block of several policies is run for each of them, in
 // turn, and each time only the rows of that one are written.  8192 rows of 4096 in
-// eight policies: 78 us at rank 128, 127 at rank 256 (207 where each block of
-// several policies read U itself).
+// eight policies: 84 us at rank 128, 141 at rank 256 (with each block of several
+// policies reading U itself half as much again).
 constexpr int kStripBlocks = 8;
 constexpr int kStripWaves = 8;
 
@@ -1026,7 +1027,13 @@ void launch_expand(const AdapterArgs& a, const AdapterPlan& p, float c, const fl
                    hipStream_t s) {
   const int64_t n_cb = (a.d + 63) / 64;
   const int64_t blocks = (a.T + 15) / 16;
-  // eight blocks to a SIMD and more: walk down several with one U
+  // Eight blocks to a SIMD and more: walk down several with one U.  Both launches of
+  // a call, 4096 x 4096, eight policies, us here / by the block kernel:
+  //   rank 64     2047 rows in runs  42 /  37, mixed 141 /  60; 4096: 60 /  57, 270 / 108
+  //   rank 256    2047 rows in runs 156 / 121, mixed 531 / 190; 4096: 159 / 160, 616 / 315
+  //   rank 16     2047 rows in runs  23 /  24, mixed  36 /  34; 4096: 38 /  38,  66 /  60
+  // so in runs the two meet near 4096 rows, and batches that mix policies would be
+  // faster by blocks past that too.
   if (blocks * n_cb >= 8 * 4 * kCus) {
     if constexpr (RP <= 64 && VEC) {
       const int64_t wide = (a.d + 255) / 256;

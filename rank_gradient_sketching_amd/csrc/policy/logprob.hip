@@ -37,9 +37,9 @@
 // Bound: the stream of the logits and, close behind it, the vector unit (eight
 // elements cost about 70 issue slots, 32 of them the exponentials).  One
 // work-group per row where the rows fill the chip; fewer rows are cut into pieces
-// whose states and keys a second kernel joins.  4096 x 152064 bf16: 198 us, 6.3
-// TB/s.  8 rows of it with eight alternatives: 8.4 + 6.2 us (5.1 + 3.3 without),
-// 501 x 32003 fp32 likewise 23.0 + 5.2 (15.2 + 3.9).
+// whose states and keys a second kernel joins.  4096 x 152064 bf16: 199 us, 6.3
+// TB/s.  8 rows of it with eight alternatives: 8.9 + 6.7 us (5.4 + 3.3 without),
+// 501 x 32003 fp32 with five 23.3 + 5.5 (16.7 + 3.9 without).
 #include <math.h>
 
 #include "common.hpp"
@@ -774,8 +774,14 @@ __global__ __launch_bounds__(kThreads) void logprob_grad_kernel(LogprobGradArgs 
 }
 
 // Work-groups a chip full of streaming work wants, and the most a launch takes
-// (tasks beyond it are walked by the same work-groups).
-constexpr int64_t kFill = 512;   // (501 x 32003: 28.4 us; 1024 31.7, 2048 32.2, 4096 40)
+// (tasks beyond it are walked by the same work-groups).  Calls without alternatives
+// in us at 256, 512, 1024, 2048:
+//   300 x 32003 bf16   14   17  16  18     300 x 152064 bf16  37  32  29  31
+//   501 x 32003 fp32   15   19  20  21     501 x 152064 fp32  49  53  54  56
+//   600 x 32003 fp32   18   18  22  24    1000 x 152064 bf16  58  58  64  66
+// 512 is the middle: 256 is up to a fifth faster where a row has few pieces, and up
+// to a fifth slower on few long rows.
+constexpr int64_t kFill = 512;
 constexpr int64_t kMaxGrid = 1 << 20;
 
 template <class T>

@@ -6,6 +6,12 @@ and the rank-r updates of several policies beside the projection they share.
 Argument marshalling only, as in api.py: the work runs in the library's HIP
 kernels on the tensors' device, asynchronously on torch's current stream of
 that device.  Tensors must live on the GPU; nothing here falls back to the CPU.
+
+Autograd sees none of it, as in the rest of the library: results are detached
+(adapter_apply into Y adds no gradient of the update to Y's graph), and writes
+into given tensors raise no version counter, so a tensor that autograd has saved
+must not be one of them.  A program takes gradients by the calls themselves
+(token_logprob_backward) or wraps them in a torch.autograd.Function of its own.
 """
 import ctypes
 import functools
@@ -294,7 +300,9 @@ def adamw_step(bound, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, grad_scale=Non
     corrections b = 1 - beta^step; step counts from 1.  grad_scale: fp32 GPU
     tensor of one entry that scales every gradient (a loss scale's inverse, a
     clipping factor), read on the GPU.  For parameters that are not sketched;
-    sketch_update steps a sketch.  Returns None."""
+    sketch_update steps a sketch.  A captured call replays its lr and step: with
+    8-bit states the same dither each time, which rounds with a bias, so those
+    are stepped outside the graph.  Returns None."""
     if not isinstance(bound, _Bound):
         raise TypeError("bound must be a handle of adamw_bind")
     dev = bound.table_dev.get_device()
