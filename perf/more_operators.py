@@ -388,8 +388,8 @@ def _own(st):
                            per_tensor=True)
         if st["clip"]:
             lg.grad_clip(st["bound"], res.scale)
-            return [res.norm[0], res.scale, res.norms] + [st["out"][kind] for kind in st["flat"]]
-        return [res.norm[0], res.scale, res.norms]
+            return [res.norm, res.scale, res.norms] + [st["out"][kind] for kind in st["flat"]]
+        return [res.norm, res.scale, res.norms]
     act = None if st["act"] == "none" else st["act"]
     if st["op"] == "linear":
         lg.linear(st["X"], st["W"], bias=st["bias"], act=act, residual=st["residual"],
