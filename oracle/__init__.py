@@ -42,7 +42,9 @@ Parity status per function:
       and Adam rules used here are pinned against closed forms only.
   logprob, adamw, adapter (the operators around the sketch in a policy step):
       textbook definitions, pinned against closed forms and differences.
+  sample, linear, gradnorm (the operators that close a policy step): likewise.
 """
 
 from . import bf16, philox, projection, sketch, merge, kl, optim  # noqa: F401
 from . import logprob, adamw, adapter  # noqa: F401
+from . import sample, linear, gradnorm  # noqa: F401

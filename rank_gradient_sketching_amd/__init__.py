@@ -17,4 +17,8 @@ from .api import (GAUSSIAN, MAX_SHARED, MAX_SWEEP, RADEMACHER, SKETCH_OVERWRITE,
 from .policy import (MAX_TOP, STATE_BLOCK, TokenLogprob, adamw_bind,  # noqa: F401
                      adamw_state_values, adamw_step, adapter_apply, adapter_ws_bytes,
                      token_logprob, token_logprob_backward, token_logprob_ws_bytes)
+from .step import (ACTIVATIONS, GradNorm, SampledTokens, grad_clip, grad_norm,  # noqa: F401
+                   grad_norm_bind, linear, linear_backward_act, linear_backward_act_ws_bytes,
+                   linear_backward_input, linear_backward_weight, linear_ws_bytes,
+                   sample_tokens, sample_tokens_ws_bytes)
 from . import sync  # noqa: F401,E402

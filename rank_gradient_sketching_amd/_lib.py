@@ -12,6 +12,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "liblogra.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "logra.h")
 POLICY_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "logra_policy.h")
+STEP_HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "logra_step.h")
 
 _lib = None
 
@@ -138,6 +139,37 @@ SIGNATURES.update({
     "logra_adapter_apply": (ctypes.c_int, [c_vp, _i64, c_vp, _i64, c_vp, _i64, _i64, _i64, _i64,
                                            _i32, _i64, c_vp, c_vp, ctypes.c_int, c_vp, c_vp, _i64,
                                            c_vp, c_vp, _sz, c_vp]),
+})
+
+
+class GradItem(ctypes.Structure):
+    """logra_grad_item of include/logra_step.h (field for field)."""
+    _fields_ = [("g", c_vp), ("out", c_vp), ("n", ctypes.c_int64), ("g_type", ctypes.c_int32),
+                ("out_type", ctypes.c_int32)]
+
+
+_int = ctypes.c_int
+# include/logra_step.h
+SIGNATURES.update({
+    "logra_sample_tokens_ws_bytes": (_sz, [_i64, _i64]),
+    "logra_sample_tokens": (_int, [c_vp, _int, _i64, _i64, _i64, c_vp, _f32, _i32, _f32, _f32,
+                                   c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, _sz,
+                                   c_vp]),
+    "logra_grad_table_bytes": (_sz, [_i32]),
+    "logra_grad_table": (_int, [_i32, ctypes.POINTER(GradItem), c_vp, _sz]),
+    "logra_grad_norm_ws_bytes": (_sz, [c_vp]),
+    "logra_grad_norm": (_int, [c_vp, c_vp, _int, _f64, c_vp, c_vp, c_vp, c_vp, c_vp, _sz, c_vp]),
+    "logra_grad_clip": (_int, [c_vp, c_vp, c_vp, c_vp]),
+    "logra_linear_ws_bytes": (_sz, [_i64, _i64, _i64]),
+    "logra_linear_backward_act_ws_bytes": (_sz, [_i64, _i64]),
+    "logra_linear": (_int, [c_vp, _i64, c_vp, _i64, _i64, _i64, _i64, c_vp, _int, _int, c_vp, _i64,
+                            c_vp, _int, _i64, c_vp, _i64, c_vp, _sz, c_vp]),
+    "logra_linear_backward_act": (_int, [c_vp, _int, _i64, c_vp, _i64, _int, _i64, _i64, c_vp, _i64,
+                                         c_vp, c_vp, _sz, c_vp]),
+    "logra_linear_backward_input": (_int, [c_vp, _i64, c_vp, _i64, _i64, _i64, _i64, c_vp, _i64,
+                                           c_vp, _i64, c_vp, _sz, c_vp]),
+    "logra_linear_backward_weight": (_int, [c_vp, _i64, c_vp, _i64, _i64, _i64, _i64, _int, c_vp,
+                                            _int, _i64, c_vp, _sz, c_vp]),
 })
 
 OK, EINVAL, EWORKSPACE, EHIP = 0, -1, -2, -3

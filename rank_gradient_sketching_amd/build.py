@@ -21,7 +21,8 @@ ARCH = "gfx950"
 
 SOURCES = ["abi.cpp", "regen.hip", "sketch.hip", "merge.hip", "kl.hip", "kl_sweep.hip", "optim.hip",
            "noalloc.hip", "policy/abi_policy.cpp", "policy/logprob.hip", "policy/adamw.hip",
-           "policy/adapter.hip"]
+           "policy/adapter.hip", "step/abi_step.cpp", "step/sample.hip", "step/norm.hip",
+           "step/linear.hip"]
 
 
 def hipcc():

@@ -1,0 +1,252 @@
+"""logra_sample_tokens on the GPU against the fp64 oracle.
+
+The token and the number kept are whole numbers and have to be equal: both sides
+form masses to about 1e-14 and a draw (or a top-p border) lies nearer than that to
+a border of the cumulative masses once in 10^9 rows.  logp and logq are one rounding
+to fp32 of a value whose fp64 terms carry 1e-14: u |x| + 1e-7 of slack below, u = 2^-24.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import sample as osample
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+BELOW_1 = 1 - 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def lg():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import rank_gradient_sketching_amd as m
+    return m
+
+
+def padded(t, extra=0):
+    """GPU copy whose rows have a stride of whole 16-byte groups; NaN behind them."""
+    n, V = t.shape
+    buf = torch.full((n, -(-V // 8) * 8 + 8 * extra), float("nan"), dtype=t.dtype, device="cuda")
+    buf[:, :V] = t.cuda()
+    return buf[:, :V]
+
+
+def logits(n, V, dtype, seed=0, scale=3.0):
+    rng = np.random.default_rng([seed, n, V])
+    z = rng.standard_normal((n, V), dtype=np.float32) * np.float32(scale)
+    return torch.from_numpy(z).to(DT[dtype])
+
+
+def uniform(n, seed=0):
+    return torch.from_numpy(np.random.default_rng([seed, 7, n]).random(n, dtype=np.float32))
+
+
+def f32(x):
+    return x if isinstance(x, torch.Tensor) else float(np.float32(x))
+
+
+def check(lg, z, u, **kw):
+    """Runs both sides on the same logits and compares all four results."""
+    gpu = {k: v.cuda() if isinstance(v, torch.Tensor) else v for k, v in kw.items()}
+    got = lg.sample_tokens(padded(z), u.cuda(), **gpu)
+    ref = osample.rows(z.double().numpy(), u.numpy().astype(np.float64),
+                       **{k: f32(v).numpy() if isinstance(v, torch.Tensor) else f32(v)
+                          if k != "top_k" else v for k, v in kw.items()})
+    torch.cuda.synchronize()
+    assert np.array_equal(got.kept.cpu().numpy(), ref[3]), (got.kept.cpu().numpy()[:9], ref[3][:9])
+    assert np.array_equal(got.token.cpu().numpy(), ref[0])
+    for a, b in ((got.logp, ref[1]), (got.logq, ref[2])):
+        a = a.cpu().numpy().astype(np.float64)
+        assert np.array_equal(np.isnan(a), np.isnan(b))
+        ok = ~np.isnan(b)
+        assert np.all(np.abs(a[ok] - b[ok]) <= U * np.abs(b[ok]) + 1e-7)
+    return got
+
+
+SETTINGS = [dict(), dict(tau=0.7), dict(top_k=1), dict(top_k=50, top_p=0.95), dict(top_p=0.5),
+            dict(min_p=0.05), dict(tau=1.3, top_k=700, top_p=0.9, min_p=0.01), dict(min_p=1.0),
+            dict(top_p=BELOW_1), dict(top_k=3, tau=0.05)]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("n,V", [(1, 1), (2, 7), (5, 8), (9, 1000), (33, 4099), (3, 32003),
+                                 (2, 152064)])
+@pytest.mark.parametrize("kw", SETTINGS, ids=str)
+def test_matches_the_oracle(lg, n, V, dtype, kw):
+    check(lg, logits(n, V, dtype), uniform(n), **kw)
+
+
+@pytest.mark.parametrize("n", [200, 300, 600])
+def test_many_rows(lg, n):
+    check(lg, logits(n, 2500, "bf16", 3), uniform(n, 3), top_k=40, top_p=0.9)
+    check(lg, logits(n, 1200, "fp32", 4), uniform(n, 4), tau=0.8)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_settings_of_each_row(lg, dtype):
+    n, V = 64, 5000
+    rng = np.random.default_rng(11)
+    pick = lambda v, t: torch.from_numpy(rng.choice(v, n).astype(t))
+    u = uniform(n, 5)
+    u[::7] = -1.0
+    check(lg, logits(n, V, dtype, 5), u, tau=pick([0.5, 1.0, 1.7], np.float32),
+          top_k=pick([0, 1, 20, 4999, 5000, 100000, -3], np.int32),
+          top_p=pick([1.0, 0.9, 0.3], np.float32), min_p=pick([0.0, 0.1], np.float32))
+
+
+def test_rows_out_of_range_have_no_token(lg):
+    n = 12
+    one = torch.ones(n)
+    tau, top_p, min_p, u = one.clone(), one.clone(), torch.zeros(n), one * 0.5
+    tau[0], tau[1], tau[2], tau[3] = 0.0, -1.0, float("nan"), float("inf")
+    top_p[4], top_p[5], top_p[6] = 0.0, 1.5, float("nan")
+    min_p[7], min_p[8] = -0.5, float("nan")
+    u[9], u[10] = 1.0, float("nan")          # left out: no number in [0, 1)
+    got = check(lg, logits(n, 100, "bf16"), u, tau=tau, top_p=top_p, min_p=min_p)
+    assert got.token[:11].eq(-1).all() and got.token[11] >= 0
+    assert got.logp[:9].isnan().all() and got.logp[9:11].eq(0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_ties_go_by_index(lg, dtype):
+    # few distinct values: hundreds of tokens share a logit, at every border
+    rng = np.random.default_rng(2)
+    z = torch.from_numpy(rng.integers(-3, 4, (40, 3001)).astype(np.float32)).to(DT[dtype])
+    z[0] = 1.25                                # all equal
+    z[1] = -0.0
+    z[1, ::2] = 0.0                            # zeros of both signs are equal
+    z[2] = -1e4
+    u = uniform(40, 6)
+    for kw in (dict(), dict(top_k=100), dict(top_p=0.37), dict(min_p=0.3)):
+        check(lg, z, u, **kw)
+    u[:] = BELOW_1
+    check(lg, z, u)
+    u[:] = 0.0
+    got = check(lg, z, u)
+    assert got.token[0] == 0 and got.token[1] == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_flat_rows(lg, dtype):
+    # an untrained model's logits: all within a fraction of a bin's width, so that
+    # the keys are binned again, and (fp32) a third time
+    for scale in (1e-1, 1e-3, 1e-6):
+        z = 5.0 + logits(4, 152064, "fp32", 8, scale)
+        for kw in (dict(), dict(top_k=5000, top_p=0.5)):
+            check(lg, z.to(DT[dtype]), uniform(4, 8), **kw)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_masks_and_extremes(lg, dtype):
+    z = logits(14, 2000, dtype, 9)
+    lowest = torch.finfo(z.dtype).min
+    z[0, 3:] = -float("inf")                  # three tokens left
+    z[1, :] = -float("inf")                   # none
+    z[2, :-1] = -float("inf")                 # one, the last
+    z[3, 77] = float("nan")
+    z[4, 78] = float("inf")
+    z[5, 5:] = lowest                         # finite masks
+    z[6] = lowest                             # all of them
+    z[7, ::2] = -1e30
+    z[8] = z[8] * 1e30                        # peaks far apart
+    z[9, 9] = torch.finfo(z.dtype).max
+    z[10, 1:] = z[10, 1:] - 200               # one token has all the mass
+    z[11] = z[11] + 1e6
+    z[12, 0], z[12, 1:] = 60.0, 0.0
+    u = uniform(14, 9)
+    for kw in (dict(), dict(top_k=10), dict(top_p=0.9), dict(min_p=1e-3), dict(top_k=1500),
+               dict(min_p=1e-38), dict(tau=1e-30), dict(tau=1e30), dict(tau=2.0 ** -140)):
+        got = check(lg, z, u, **kw)
+        assert got.token[1] == -1 and got.logp[1].isnan() and got.token[2] == 1999
+    u[:] = BELOW_1
+    check(lg, z, u)
+    u[:] = 0.0
+    got = check(lg, z, u)
+    keep = [i for i in range(14) if i not in (1, 3, 4)]
+    best = z.float()[keep].numpy().argmax(1)   # (the first of equal ones)
+    assert np.array_equal(got.token.cpu().numpy()[keep], best)
+
+
+def test_logp_is_token_logprobs(lg):
+    z, u = logits(50, 6000, "bf16", 12), uniform(50, 12)
+    zz = padded(z)
+    got = lg.sample_tokens(zz, u.cuda(), tau=0.8, top_k=30)
+    ref = lg.token_logprob(zz, got.token, tau=0.8)
+    # token_logprob: R + 4 u (|logp| + ln V), R = u (ceil(V / 256) + 160)
+    assert (got.logp - ref.logp).abs().max().item() < U * (184 + 4 * 40)
+    assert torch.all(got.logq >= got.logp)
+
+
+def test_draws_have_the_distribution(lg):
+    """u on an even grid: each kept token is drawn p_j / M of the time, to one draw."""
+    n, V = 4096, 300
+    z = logits(1, V, "fp32", 13, 1.0)
+    u = ((torch.arange(n) + 0.5) / n)
+    got = lg.sample_tokens(padded(z.expand(n, V)), u.cuda(), top_p=0.9)
+    K = int(got.kept[0])
+    p = np.sort(np.exp(z[0].double().numpy()))[::-1][:K]
+    order = np.argsort(-z[0].double().numpy(), kind="stable")[:K]
+    count = np.bincount(got.token.cpu().numpy(), minlength=V)
+    assert count.sum() == count[order].sum() == n
+    assert np.all(np.abs(count[order] - n * p / p.sum()) <= 1)
+
+
+def test_given_outputs_and_bits(lg):
+    z, u = padded(logits(31, 20000, "bf16", 14), 3), uniform(31, 14).cuda()
+    a = lg.sample_tokens(z, u, top_p=0.9)
+    out = lg.SampledTokens(torch.full((31,), -7, device="cuda"), None, None, None)
+    assert lg.sample_tokens(z, u, top_p=0.9, out=out) is out
+    assert torch.equal(out.token, a.token)
+    for _ in range(3):
+        b = lg.sample_tokens(z, u, top_p=0.9)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+    e = lg.sample_tokens(z[:0], u[:0])
+    assert all(x.numel() == 0 for x in e)
+
+
+def test_long_stride(lg):
+    """Row offsets past 2^31 elements."""
+    V, ld = 1000, (1 << 30) + 8
+    buf = torch.empty(2 * ld + 1024, dtype=torch.bfloat16, device="cuda")
+    z = buf.as_strided((3, V), (ld, 1))
+    zz = logits(3, V, "bf16", 15)
+    z.copy_(zz)
+    u = uniform(3, 15)
+    got = lg.sample_tokens(z, u.cuda(), top_k=9)
+    ref = osample.rows(zz.double().numpy(), u.numpy().astype(np.float64), top_k=9)
+    assert np.array_equal(got.token.cpu().numpy(), ref[0])
+
+
+def test_graph_and_streams(lg):
+    zs = [padded(logits(8, 30000, "bf16", s)) for s in (16, 17)]
+    u = uniform(8, 16).cuda()
+    ref = [lg.sample_tokens(z, u, top_p=0.8) for z in zs]
+    torch.cuda.synchronize()
+    ws = torch.empty(max(256, lg.sample_tokens_ws_bytes(8, 30000)), dtype=torch.uint8,
+                     device="cuda")
+    out = lg.SampledTokens(*(torch.empty_like(x) for x in ref[0]))
+    g = torch.cuda.CUDAGraph()
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        lg.sample_tokens(zs[0], u, top_p=0.8, out=out, ws=ws)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        lg.sample_tokens(zs[0], u, top_p=0.8, out=out, ws=ws)
+    for rep in range(4):
+        for x in out:
+            x.zero_()
+        lg.sample_tokens(zs[1], u, top_p=0.8, ws=ws)     # eager work through the same scratch
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, ref[0])), rep
+    streams = [torch.cuda.Stream() for _ in zs]
+    got = []
+    for z, q in zip(zs, streams):
+        with torch.cuda.stream(q):
+            got.append(lg.sample_tokens(z, u, top_p=0.8))
+    torch.cuda.synchronize()
+    for a, b in zip(got, ref):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
