@@ -173,7 +173,8 @@ size_t logra_linear_backward_act_ws_bytes(int64_t T, int64_t d);
  * Columns past d are not written.
  * ws: device scratch of logra_linear_ws_bytes(T, d, k) bytes, 256-B aligned (not
  *     inspected when that is 0).
- * No other overlap.  T == 0 is a no-op.  d, k >= 1; T, d, k < 2^31.
+ * No other overlap.  T == 0 is a no-op.  d, k >= 1; T, d, k < 2^31; results past what
+ * one launch covers (about T d = 5 10^11) are refused.
  * Returns LOGRA_OK, LOGRA_EINVAL, LOGRA_EWORKSPACE or LOGRA_EHIP.
  */
 int logra_linear(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw, int64_t T,

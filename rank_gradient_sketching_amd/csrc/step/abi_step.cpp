@@ -220,6 +220,7 @@ int logra_linear(const uint16_t* X, int64_t ldx, const uint16_t* W, int64_t ldw,
   if (!matrix_ok(X, ldx, k, LOGRA_BF16) || !matrix_ok(W, ldw, k, LOGRA_BF16) ||
       !matrix_ok(out, ldo, d, out_type))
     return LOGRA_EINVAL;
+  if (!logra::gemm_fits(logra::GemmForm::kForward, T, d, k)) return LOGRA_EINVAL;
   const size_t need = logra::gemm_ws_bytes(logra::GemmForm::kForward, T, d, k);
   if (!ws_ok(need, ws, ws_bytes)) return LOGRA_EWORKSPACE;
   const Span o = span(out, T, d, ldo, bytes_of(out_type)), r = span(residual, T, d, ldr, 2);
@@ -296,6 +297,7 @@ int logra_linear_backward_input(const uint16_t* dY, int64_t ldy, const uint16_t*
   if (!matrix_ok(dY, ldy, d, LOGRA_BF16) || !matrix_ok(W, ldw, k, LOGRA_BF16) ||
       !matrix_ok(dX, ldx, k, LOGRA_BF16))
     return LOGRA_EINVAL;
+  if (!logra::gemm_fits(logra::GemmForm::kInput, T, k, d)) return LOGRA_EINVAL;
   const size_t need = logra::gemm_ws_bytes(logra::GemmForm::kInput, T, k, d);
   if (!ws_ok(need, ws, ws_bytes)) return LOGRA_EWORKSPACE;
   const Span o = span(dX, T, k, ldx, 2), w = span(need ? ws : nullptr, 1, (int64_t)need, 0, 1);
@@ -330,6 +332,7 @@ int logra_linear_backward_weight(const uint16_t* dY, int64_t ldy, const uint16_t
   if (T == 0 && flags != 0) return LOGRA_OK;
   if (T > 0 && (!matrix_ok(dY, ldy, d, LOGRA_BF16) || !matrix_ok(X, ldx, k, LOGRA_BF16)))
     return LOGRA_EINVAL;
+  if (!logra::gemm_fits(logra::GemmForm::kWeight, d, k, T)) return LOGRA_EINVAL;
   const size_t need = T > 0 ? logra::gemm_ws_bytes(logra::GemmForm::kWeight, d, k, T) : 0;
   if (!ws_ok(need, ws, ws_bytes)) return LOGRA_EWORKSPACE;
   const Span o = span(dW, d, k, ldw, bytes_of(dw_type));

@@ -88,6 +88,8 @@ struct GemmArgs {
   int64_t ldpre;
 };
 enum class GemmForm { kForward, kInput, kWeight };   // A, B along k: neither; B; both
+// Whether a product fits a launch.
+bool gemm_fits(GemmForm form, int64_t M, int64_t N, int64_t K);
 size_t gemm_ws_bytes(GemmForm form, int64_t M, int64_t N, int64_t K);
 hipError_t launch_gemm(GemmForm form, const GemmArgs& a, char* ws, hipStream_t s);
 
