@@ -12,11 +12,18 @@
 // bits for vocabularies past 2^18), so the sums are exact and do not depend on the
 // order of the atomics, while every token keeps a relative precision of 2^-46
 // whatever its octave.  X and the exponential (a polynomial of degree 5 on [0, 1/64)
-// of an octave, 2e-15) are fp64: a draw then hits a border of the cumulative masses
-// wrongly about once in 10^10, where fp32 masses would in one row of a hundred.
-// Scanning the bins gives the bin of a target; inside it the keys (the order-
-// preserving bits of the logits) are binned again, up to twice more, until a bin
-// holds one logit, whose tokens then go by their index.
+// of an octave, 2e-15) are fp64, which costs a fused step what fp32 does: a draw then
+// hits a border of the cumulative masses wrongly about once in 10^10, where fp32
+// masses would in one row of a hundred.
+// Scanning the bins gives, for each target, the bin (or, where a target depends on
+// one that is not resolved yet, the few bins) that it lies in.  Their tokens, usually
+// some tens, are gathered from the row, sorted by logit and index, and resolve all
+// targets at once.  A row whose bins hold more than fit there (logits nearly equal, or
+// many ties) takes them one by one: the keys (the order-preserving bits of the logits)
+// of a bin are binned again, up to three times, until one logit is left, whose tokens
+// then go by their index.
+//
+// @@BOUND@@
 #include <math.h>
 
 #include "common.hpp"
@@ -29,11 +36,11 @@ namespace {
 
 typedef unsigned long long u64;
 
-constexpr int kThreads = 1024;
-constexpr int kWaves = kThreads / 64;
 constexpr int kBins = 4096;
-constexpr int kPer = kBins / kThreads;     // bins of a thread in a scan
 constexpr double kFar = (double)kBins;     // X of tokens that only count
+constexpr int kList = 2048;                // tokens that are gathered and sorted
+constexpr int kSubs = 1024;                // bins of a refinement
+constexpr int kMaxWaves = 16;
 
 template <bool F32>
 struct Row {
@@ -47,32 +54,30 @@ template <bool F32>
 __device__ __forceinline__ void logits_of(const u32x4& q, int v, int V, float* z) {
   constexpr int E = Row<F32>::kE;
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
+  for (int e = 0; e < E; ++e)
     z[e] = F32 ? __uint_as_float(q[e & 3]) : (e & 1) ? bf16_hi(q[e >> 1]) : bf16_lo(q[e >> 1]);
-  }
-  if (__builtin_expect((v + 1) * E > V, 0)) {
+  if (__builtin_expect((uint32_t)(v + 1) * E > (uint32_t)V, 0)) {
 #pragma unroll
     for (int e = 0; e < E; ++e)
-      if (v * E + e >= V) z[e] = -INFINITY;
+      if ((uint32_t)v * E + e >= (uint32_t)V) z[e] = -INFINITY;
   }
 }
 
-// f(z, index) for every logit of the row.
-template <bool F32, class F>
-__device__ __forceinline__ void for_each(const Row<F32>& r, F f) {
+// f(z, index) for the logits of vectors [v0, v1) of the row, U loads in flight.
+template <int THREADS, int U, bool F32, class F>
+__device__ __forceinline__ void for_each(const Row<F32>& r, int v0, int v1, F f) {
   constexpr int E = Row<F32>::kE;
-  constexpr int U = 4;
-  for (int v0 = (int)threadIdx.x; v0 < r.n_vec; v0 += U * kThreads) {
+  for (int at = v0 + (int)threadIdx.x; at < v1; at += U * THREADS) {
     u32x4 q[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int v = v0 + i * kThreads;
-      q[i] = r.p[v < r.n_vec ? v : v0];
+      const int v = at + i * THREADS;
+      q[i] = r.p[v < v1 ? v : at];
     }
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int v = v0 + i * kThreads;
-      if (v < r.n_vec) {
+      const int v = at + i * THREADS;
+      if (v < v1) {
         float z[E];
         logits_of<F32>(q[i], v, r.V, z);
 #pragma unroll
@@ -91,12 +96,24 @@ __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key ^ ((key & 0x80000000u) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-// What a row's weights are formed with.
+// What a row's weights are formed with.  X = z (-l64) + m l64 in one fused step: the
+// rounding of m l64 is common to all tokens and cancels in every ratio of masses (x0,
+// the largest logit's own X, is that rounding).
 struct Scale {
-  double m, l64;      // largest logit, 64 log2(e) / tau
+  double l64, c, x0;  // 64 log2(e) / tau, m l64
   double unit;        // 2^bits, bits of a weight's integer
 };
-__device__ __forceinline__ double x_of(float z, const Scale& c) { return (c.m - (double)z) * c.l64; }
+__device__ __forceinline__ Scale scale_of(float m, float tau, double unit) {
+  Scale s;
+  s.l64 = 64.0 * 1.4426950408889634074 / (double)tau;
+  s.c = (double)m * s.l64;
+  s.x0 = fma((double)m, -s.l64, s.c);
+  s.unit = unit;
+  return s;
+}
+__device__ __forceinline__ double x_of(float z, const Scale& s) {
+  return fma((double)z, -s.l64, s.c) - s.x0;
+}
 
 // round(2^(-r / 64) unit) for r in [0, 1): the series of e^t, t = -r ln(2) / 64.
 __device__ __forceinline__ u64 weight_of(double r, const Scale& c) {
@@ -116,36 +133,50 @@ __device__ __forceinline__ double step_of(int b, const Scale& c) {
   return exp2(-(double)b / 64.0) / c.unit;
 }
 
-// LDS of a row.  cum and num hold the bins' cumulative masses and numbers once
-// scanned; mass and cnt are the bins while they fill (again for each refinement).
+// LDS of a row, 65 KB, so that two rows share a CU and one's loads cover the other's
+// arithmetic.
 struct Lds {
-  u64 mass[kBins];
-  uint32_t cnt[kBins];
-  double cum[kBins];
-  uint32_t num[kBins];
-  double wave_d[kWaves];
-  u64 wave_q[kWaves];
-  uint32_t wave_u[kWaves], wave_v[kWaves];
-  uint32_t found;
-  double at_d;
-  uint32_t at_u;
-  u64 at_q;
+  union {
+    u64 mass[kBins];         // while the bins fill
+    double cum[kBins];       // then: cumulative masses
+  };
+  uint32_t num[kBins];       // numbers of tokens, then cumulative
+  union {
+    u64 list[kList];         // ~key, index
+    struct {
+      u64 mass[kSubs];
+      uint32_t num[kSubs];
+    } sub;
+  };
+  union {
+    double wave_d[kMaxWaves];
+    u64 wave_q[kMaxWaves];
+  };
+  uint32_t wave_u[kMaxWaves];
+  double at_mass[2];
+  uint32_t at_rank[2], at_key, n_list;
+  int at_index;
 };
 
 // ------------------------------------------------------------------ over the work-group
-template <class T, class F>
+template <int THREADS, class T, class F>
 __device__ __forceinline__ T reduce(T x, T* lds, F f) {
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) x = f(x, __shfl_xor(x, off));
   if (threadIdx.x % 64 == 0) lds[threadIdx.x / 64] = x;
   __syncthreads();
   x = lds[0];
-  for (int i = 1; i < kWaves; ++i) x = f(x, lds[i]);
+#pragma unroll
+  for (int i = 1; i < THREADS / 64; ++i) x = f(x, lds[i]);
   __syncthreads();
   return x;
 }
+struct Add {
+  template <class T>
+  __device__ T operator()(T a, T b) const { return a + b; }
+};
 // Sum over the threads before this one (a fixed order).
-template <class T>
+template <int THREADS, class T>
 __device__ __forceinline__ T before_me(T x, T* lds) {
   T incl = x;
 #pragma unroll
@@ -156,7 +187,9 @@ __device__ __forceinline__ T before_me(T x, T* lds) {
   if (threadIdx.x % 64 == 63) lds[threadIdx.x / 64] = incl;
   __syncthreads();
   T base = 0;
-  for (int i = 0; i < (int)(threadIdx.x / 64); ++i) base += lds[i];
+#pragma unroll
+  for (int i = 0; i < THREADS / 64; ++i)
+    if (i < (int)(threadIdx.x / 64)) base += lds[i];
   __syncthreads();
   const T up = __shfl_up(incl, 1);
   return base + (threadIdx.x % 64 ? up : T(0));
@@ -180,36 +213,31 @@ struct Place {
   int index;
 };
 
-// First of n entries that meets the target; -1 where none does.  at(b) gives the pair
+// First of N entries that meets the target; -1 where none does.  at(b) gives the pair
 // (mass, number) up to and including entry b.
-template <class F>
+template <int THREADS, int N, class F>
 __device__ __forceinline__ int first_met(Lds& s, const Target& t, F at) {
-  if (threadIdx.x == 0) s.found = 0xFFFFFFFFu;
-  __syncthreads();
+  constexpr int kPer = N / THREADS;
+  uint32_t f = 0xFFFFFFFFu;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
+  for (int i = kPer - 1; i >= 0; --i) {
     const int b = (int)threadIdx.x * kPer + i;
     double c;
     uint32_t n;
     at(b, &c, &n);
-    if (t.met(c, n)) {
-      atomicMin(&s.found, (uint32_t)b);
-      break;
-    }
+    if (t.met(c, n)) f = (uint32_t)b;
   }
-  __syncthreads();
-  const uint32_t f = s.found;
-  __syncthreads();
-  return f == 0xFFFFFFFFu ? -1 : (int)f;
+  return (int)reduce<THREADS>(f, s.wave_u, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
 }
 
+// ------------------------------------------------------------------ one target at a time
 // The j-th token (j >= 1, by index) with logit key `key`.
-template <bool F32>
-__device__ int nth_equal(const Row<F32>& r, Lds& s, uint32_t key, uint32_t j) {
+template <int THREADS, bool F32>
+__device__ __noinline__ int nth_equal(Row<F32> r, Lds& s, uint32_t key, uint32_t j) {
   constexpr int E = Row<F32>::kE;
   uint32_t done = 0;
-  if (threadIdx.x == 0) s.found = 0;
-  for (int v0 = 0; v0 < r.n_vec; v0 += kThreads) {
+  if (threadIdx.x == 0) s.at_index = 0;
+  for (int v0 = 0; v0 < r.n_vec; v0 += THREADS) {
     const int v = v0 + (int)threadIdx.x;
     uint32_t mine = 0, bits = 0;
     if (v < r.n_vec) {
@@ -222,32 +250,33 @@ __device__ int nth_equal(const Row<F32>& r, Lds& s, uint32_t key, uint32_t j) {
           bits |= 1u << e;
         }
     }
-    const uint32_t before = done + before_me(mine, s.wave_u);
+    const uint32_t before = done + before_me<THREADS>(mine, s.wave_u);
     if (before < j && before + mine >= j) {
       uint32_t left = j - before;
       int e = 0;
       for (;; ++e)
         if ((bits >> e & 1) && --left == 0) break;
-      s.found = (uint32_t)(v * E + e);
+      s.at_index = v * E + e;
     }
-    done += reduce(mine, s.wave_u, [](uint32_t a, uint32_t b) { return a + b; });
+    done += reduce<THREADS>(mine, s.wave_u, Add());
     if (done >= j) break;       // (the same in every thread)
   }
   __syncthreads();
-  const int f = (int)s.found;
+  const int f = s.at_index;
   __syncthreads();
   return f;
 }
 
 // The place inside bin b where the order meets a target that the bin meets: the bin's
 // keys are binned again until one key is left.
-template <bool F32>
-__device__ Place refine(const Row<F32>& r, Lds& s, const Scale& c, int b, const Target& t,
-                        bool want_index) {
+template <int THREADS, bool F32>
+__device__ __noinline__ Place refine(Row<F32> r, Lds& s, Scale c, int b, Target t,
+                                     bool want_index) {
+  constexpr int kPer = kSubs / THREADS;
   const double before = b ? s.cum[b - 1] : 0.0, step = step_of(b, c);
   const uint32_t n_before = b ? s.num[b - 1] : 0u;
   uint32_t lo = 0xFFFFFFFFu, hi = 0;
-  for_each<F32>(r, [&](float z, int) {
+  for_each<THREADS, 4>(r, 0, r.n_vec, [&](float z, int) {
     const double X = x_of(z, c);
     if (X < kFar && (int)X == b) {
       const uint32_t k = key_of(z);
@@ -255,25 +284,25 @@ __device__ Place refine(const Row<F32>& r, Lds& s, const Scale& c, int b, const 
       hi = k > hi ? k : hi;
     }
   });
-  lo = reduce(lo, s.wave_u, [](uint32_t x, uint32_t y) { return x < y ? x : y; });
-  hi = reduce(hi, s.wave_u, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
+  lo = reduce<THREADS>(lo, s.wave_u, [](uint32_t x, uint32_t y) { return x < y ? x : y; });
+  hi = reduce<THREADS>(hi, s.wave_u, [](uint32_t x, uint32_t y) { return x > y ? x : y; });
   u64 q_done = 0;
   uint32_t n_done = 0;
   for (;;) {
     const uint32_t range = hi - lo;
-    const int shift = range < (uint32_t)kBins ? 0 : 32 - __clz((int)range) - 12;
-    for (int i = (int)threadIdx.x; i < kBins; i += kThreads) {
-      s.mass[i] = 0;
-      s.cnt[i] = 0;
+    const int shift = range < (uint32_t)kSubs ? 0 : 32 - __clz((int)range) - 10;
+    for (int i = (int)threadIdx.x; i < kSubs; i += THREADS) {
+      s.sub.mass[i] = 0;
+      s.sub.num[i] = 0;
     }
     __syncthreads();
-    for_each<F32>(r, [&](float z, int) {
+    for_each<THREADS, 4>(r, 0, r.n_vec, [&](float z, int) {
       const double X = x_of(z, c);
       const uint32_t k = key_of(z);
       if (X < kFar && (int)X == b && k >= lo && k <= hi) {
         const uint32_t sub = (hi - k) >> shift;
-        atomicAdd(&s.mass[sub], weight_of(X - (double)b, c));
-        atomicAdd(&s.cnt[sub], 1u);
+        atomicAdd(&s.sub.mass[sub], weight_of(X - (double)b, c));
+        atomicAdd(&s.sub.num[sub], 1u);
       }
     });
     __syncthreads();
@@ -282,28 +311,29 @@ __device__ Place refine(const Row<F32>& r, Lds& s, const Scale& c, int b, const 
     uint32_t n[kPer], ns = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      q[i] = qs += s.mass[threadIdx.x * kPer + i];
-      n[i] = ns += s.cnt[threadIdx.x * kPer + i];
+      q[i] = qs += s.sub.mass[threadIdx.x * kPer + i];
+      n[i] = ns += s.sub.num[threadIdx.x * kPer + i];
     }
-    const u64 q0 = q_done + before_me(qs, s.wave_q);
-    const uint32_t n0 = n_done + before_me(ns, s.wave_u);
+    const u64 q0 = q_done + before_me<THREADS>(qs, s.wave_q);
+    const uint32_t n0 = n_done + before_me<THREADS>(ns, s.wave_u);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      s.mass[threadIdx.x * kPer + i] = q0 + q[i];
-      s.cnt[threadIdx.x * kPer + i] = n0 + n[i];
+      s.sub.mass[threadIdx.x * kPer + i] = q0 + q[i];
+      s.sub.num[threadIdx.x * kPer + i] = n0 + n[i];
     }
     __syncthreads();
     auto subs = [&](int i, double* m, uint32_t* k) {
-      *m = before + step * (double)s.mass[i];
-      *k = n_before + s.cnt[i];
+      *m = before + step * (double)s.sub.mass[i];
+      *k = n_before + s.sub.num[i];
     };
-    int sub = first_met(s, t, subs);
+    int sub = first_met<THREADS, kSubs>(s, t, subs);
     if (sub < 0)    // (a mass that a rounding of the last sum leaves unmet: the last key)
-      sub = first_met(s, Target{kCount, n_before + s.cnt[kBins - 1], 0.0}, subs);
-    const u64 q_to = s.mass[sub];
-    const uint32_t n_to = s.cnt[sub];
-    const u64 q_from = sub ? s.mass[sub - 1] : q_done;
-    const uint32_t n_from = sub ? s.cnt[sub - 1] : n_done;
+      sub = first_met<THREADS, kSubs>(s, Target{kCount, n_before + s.sub.num[kSubs - 1], 0.0},
+                                      subs);
+    const u64 q_to = s.sub.mass[sub];
+    const uint32_t n_to = s.sub.num[sub];
+    const u64 q_from = sub ? s.sub.mass[sub - 1] : q_done;
+    const uint32_t n_from = sub ? s.sub.num[sub - 1] : n_done;
     __syncthreads();
     if (shift == 0) {
       const uint32_t key = hi - (uint32_t)sub;
@@ -320,7 +350,7 @@ __device__ Place refine(const Row<F32>& r, Lds& s, const Scale& c, int b, const 
       p.mass = before + step * (double)(q_from + w * a);
       p.rank = n_before + n_from + a;
       p.key = key;
-      p.index = want_index ? nth_equal<F32>(r, s, key, a) : -1;
+      p.index = want_index ? nth_equal<THREADS>(r, s, key, a) : -1;
       return p;
     }
     q_done = q_from;
@@ -331,135 +361,554 @@ __device__ Place refine(const Row<F32>& r, Lds& s, const Scale& c, int b, const 
   }
 }
 
-// ------------------------------------------------------------------ a row
-template <bool F32>
-__global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a, double unit) {
-  __shared__ Lds s;
-  const int64_t t = (int64_t)blockIdx.x;
-  auto put = [&](int64_t token, float logp, float logq, uint32_t kept) {
-    if (threadIdx.x != 0) return;
-    a.token[t] = token;
-    if (a.logp != nullptr) a.logp[t] = logp;
-    if (a.logq != nullptr) a.logq[t] = logq;
-    if (a.kept != nullptr) a.kept[t] = (int32_t)kept;
+// What cuts a row's order, and its draw.
+struct Cuts {
+  double p, u, total;
+  uint32_t k1, min, near;      // near: tokens in the bins
+  bool k, by_p, by_min;        // which cuts there are
+};
+// The bin where the order meets a target.
+template <int THREADS>
+__device__ __forceinline__ int bin_of(Lds& s, const Target& t, uint32_t near) {
+  auto bins = [&](int b, double* x, uint32_t* n) {
+    *x = s.cum[b];
+    *n = s.num[b];
   };
-  const float u = a.u[t];
-  if (!(u >= 0.0f && u < 1.0f)) return put(-1, 0.0f, 0.0f, 0);
-  const float tau = a.tau_rows != nullptr ? a.tau_rows[t] : a.tau;
-  const float top_p = a.top_p_rows != nullptr ? a.top_p_rows[t] : a.top_p;
-  const float min_p = a.min_p_rows != nullptr ? a.min_p_rows[t] : a.min_p;
-  const int32_t top_k = a.top_k_rows != nullptr ? a.top_k_rows[t] : a.top_k;
-  if (!(tau > 0.0f && tau < INFINITY && top_p > 0.0f && top_p <= 1.0f && min_p >= 0.0f &&
-        min_p <= 1.0f))
-    return put(-1, NAN, NAN, 0);
+  const int b = first_met<THREADS, kBins>(s, t, bins);
+  // (unmet by a rounding: the last bin that holds a token)
+  return b >= 0 ? b : first_met<THREADS, kBins>(s, Target{kCount, near, 0.0}, bins);
+}
+template <int THREADS, bool F32>
+__device__ __noinline__ Place one_by_one(Row<F32> r, Lds& s, Scale c, Cuts x, uint32_t* kept,
+                                         double* M) {
+  uint32_t k = x.k1;
+  double m = x.total;
+  // the cuts, then the draw: one loop, so that there is one copy of the search
+  Place at{};
+  for (int i = 0; i < 4; ++i) {
+    Target t{kCount, k, 0.0};
+    if (i == 0 && !x.k) continue;
+    if (i == 1) {
+      if (!x.by_p) continue;
+      t = Target{kReach, 0, x.p * m};
+    }
+    if (i == 2) {
+      if (!x.by_min || x.min >= k) continue;
+      t.count = x.min;
+    }
+    if (i == 3) t = Target{kExceed, 0, x.u * m};
+    at = refine<THREADS>(r, s, c, bin_of<THREADS>(s, t, x.near), t, i == 3);
+    if (i == 0 || (i < 3 && at.rank < k)) {
+      k = at.rank;
+      m = at.mass;
+    }
+  }
+  *kept = k;
+  *M = m;
+  return at;
+}
+
+// ------------------------------------------------------------------ a row
+struct Settings {
+  float u, tau, top_p, min_p;
+  int32_t top_k;
+  bool left_out, legal;
+};
+__device__ __forceinline__ Settings settings_of(const SampleArgs& a, int64_t t) {
+  Settings g;
+  g.u = a.u[t];
+  g.left_out = !(g.u >= 0.0f && g.u < 1.0f);
+  g.tau = a.tau_rows != nullptr ? a.tau_rows[t] : a.tau;
+  g.top_p = a.top_p_rows != nullptr ? a.top_p_rows[t] : a.top_p;
+  g.min_p = a.min_p_rows != nullptr ? a.min_p_rows[t] : a.min_p;
+  g.top_k = a.top_k_rows != nullptr ? a.top_k_rows[t] : a.top_k;
+  g.legal = g.tau > 0.0f && g.tau < INFINITY && g.top_p > 0.0f && g.top_p <= 1.0f &&
+            g.min_p >= 0.0f && g.min_p <= 1.0f;
+  return g;
+}
+struct Drawn {
+  int token;
+  float logp, logq;
+  uint32_t kept;
+};
+__device__ __forceinline__ void put(const SampleArgs& a, int64_t t, const Drawn& d) {
+  if (threadIdx.x != 0) return;
+  a.token[t] = d.token;
+  if (a.logp != nullptr) a.logp[t] = d.logp;
+  if (a.logq != nullptr) a.logq[t] = d.logq;
+  if (a.kept != nullptr) a.kept[t] = (int32_t)d.kept;
+}
+__device__ __forceinline__ Drawn left_out() { return Drawn{-1, 0.0f, 0.0f, 0}; }
+__device__ __forceinline__ Drawn no_token() { return Drawn{-1, NAN, NAN, 0}; }
+template <bool F32>
+__device__ __forceinline__ Row<F32> row_of(const SampleArgs& a, int64_t t) {
   Row<F32> r;
   r.V = a.vocab;
-  r.n_vec = (a.vocab + Row<F32>::kE - 1) / Row<F32>::kE;
-  r.p = reinterpret_cast<const u32x4*>(static_cast<const char*>(a.z) +
-                                       t * a.ld * (F32 ? 4 : 2));
-  // the largest logit; a NaN shows in `bad`
+  r.n_vec = (int)(((int64_t)a.vocab + Row<F32>::kE - 1) / Row<F32>::kE);
+  r.p = reinterpret_cast<const u32x4*>(static_cast<const char*>(a.z) + t * a.ld * (F32 ? 4 : 2));
+  return r;
+}
+
+// The largest of a thread's logits; NaN where one of them is NaN.
+template <int THREADS, bool F32>
+__device__ __forceinline__ float max_part(const Row<F32>& r, int v0, int v1) {
   float m = -INFINITY;
-  uint32_t bad = 0;
-  for_each<F32>(r, [&](float z, int) {
+  bool bad = false;
+  for_each<THREADS, 8>(r, v0, v1, [&](float z, int) {
     m = fmaxf(m, z);
-    bad |= z != z;
+    bad = bad || z != z;
   });
-  m = reduce(m, reinterpret_cast<float*>(s.wave_u), [](float x, float y) { return fmaxf(x, y); });
-  bad = reduce(bad, s.wave_u, [](uint32_t x, uint32_t y) { return x | y; });
-  if (bad || !(fabsf(m) < INFINITY)) return put(-1, NAN, NAN, 0);
-  Scale c;
-  c.m = (double)m;
-  c.l64 = 64.0 * 1.4426950408889634074 / (double)tau;
-  c.unit = unit;
-  // bins, and what only counts
-  for (int i = (int)threadIdx.x; i < kBins; i += kThreads) {
-    s.mass[i] = 0;
-    s.cnt[i] = 0;
-  }
-  __syncthreads();
+  return bad ? NAN : m;
+}
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  return a != a ? a : b != b ? b : fmaxf(a, b);
+}
+
+// Tokens that only count, and those that pass min_p.
+struct Counts {
+  uint32_t far, min;
+};
+// Fills the bins with the logits of vectors [v0, v1); a thread's own Counts.
+template <int THREADS, bool F32>
+__device__ __forceinline__ Counts bin_part(const Row<F32>& r, int v0, int v1, Lds& s,
+                                           const Scale& c, float min_p) {
+  Counts n{0, 0};
   const double x_min = min_p > 0.0f ? -64.0 * log2((double)min_p) : INFINITY;
-  uint32_t n_far = 0, n_min = 0;
-  for_each<F32>(r, [&](float z, int) {
+  for_each<THREADS, 4>(r, v0, v1, [&](float z, int) {
     if (z > -INFINITY) {
       const double X = x_of(z, c);
-      n_min += X <= x_min;
+      n.min += X <= x_min;
       if (X < kFar) {
         const int b = (int)X;
         atomicAdd(&s.mass[b], weight_of(X - (double)b, c));
-        atomicAdd(&s.cnt[b], 1u);
+        atomicAdd(&s.num[b], 1u);
       } else {
-        ++n_far;
+        ++n.far;
       }
     }
   });
-  auto sum = [](uint32_t x, uint32_t y) { return x + y; };
-  n_far = reduce(n_far, s.wave_u, sum);
-  n_min = reduce(n_min, s.wave_u, sum);
-  // cumulative masses and numbers
+  return n;
+}
+
+// Bins that hold what the targets need: single ones and runs.
+struct Wanted {
+  int lo[4], hi[4];
+  __device__ __forceinline__ bool has(int b) const {
+    return (b >= lo[0] && b <= hi[0]) || (b >= lo[1] && b <= hi[1]) ||
+           (b >= lo[2] && b <= hi[2]) || (b >= lo[3] && b <= hi[3]);
+  }
+};
+
+// Sorts the first n entries of the list (the rest is filled up with the largest).
+template <int THREADS>
+__device__ __forceinline__ void sort_list(Lds& s, int n) {
+  int size = 64;
+  while (size < n) size <<= 1;
+  for (int i = n + (int)threadIdx.x; i < size; i += THREADS) s.list[i] = ~0ull;
+  __syncthreads();
+  for (int k = 2; k <= size; k <<= 1)
+    for (int j = k >> 1; j > 0; j >>= 1) {
+      for (int i = (int)threadIdx.x; i < size / 2; i += THREADS) {
+        const int a = 2 * i - (i & (j - 1)), b = a + j;
+        const u64 x = s.list[a], y = s.list[b];
+        if ((x > y) == ((a & k) == 0)) {
+          s.list[a] = y;
+          s.list[b] = x;
+        }
+      }
+      __syncthreads();
+    }
+}
+
+// From the filled bins to the token.
+template <int THREADS, bool F32>
+__device__ __noinline__ Drawn pick(Row<F32> r, Lds& s, Scale c, Settings g, Counts all) {
+  constexpr int kPer = kBins / THREADS, kMine = kList / THREADS;
   {
+    // cumulative masses and numbers
     double d[kPer], ds = 0;
     uint32_t n[kPer], ns = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int b = (int)threadIdx.x * kPer + i;
       d[i] = ds += (double)s.mass[b] * step_of(b, c);
-      n[i] = ns += s.cnt[b];
+      n[i] = ns += s.num[b];
     }
-    const double d0 = before_me(ds, s.wave_d);
-    const uint32_t n0 = before_me(ns, s.wave_u);
+    const double d0 = before_me<THREADS>(ds, s.wave_d);
+    const uint32_t n0 = before_me<THREADS>(ns, s.wave_u);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       s.cum[threadIdx.x * kPer + i] = d0 + d[i];
       s.num[threadIdx.x * kPer + i] = n0 + n[i];
     }
+    if (threadIdx.x == 0) s.n_list = 0;
+    __syncthreads();
   }
-  __syncthreads();
   const double total = s.cum[kBins - 1];
-  const uint32_t near = s.num[kBins - 1], live = near + n_far;
-  auto bins = [&](int b, double* x, uint32_t* n) {
-    *x = s.cum[b];
-    *n = s.num[b];
-  };
-  auto find = [&](const Target& tg, bool want_index) {
-    int b = first_met(s, tg, bins);
-    if (b < 0)      // (unmet by a rounding: the last token that has a weight)
-      b = first_met(s, Target{kCount, near, 0.0}, bins);
-    return refine<F32>(r, s, c, b, tg, want_index);
-  };
-  auto mass_of = [&](uint32_t k) {
-    return k >= near ? total : find(Target{kCount, k, 0.0}, false).mass;
-  };
-  const uint32_t k1 = top_k > 0 && (uint32_t)top_k < live ? (uint32_t)top_k : live;
-  const double m1 = mass_of(k1);
+  const uint32_t near = s.num[kBins - 1], live = near + all.far;
+  auto mass_before = [&](int b) { return b > 0 ? s.cum[b - 1] : 0.0; };
+  auto num_before = [&](int b) { return b > 0 ? s.num[b - 1] : 0u; };
+
+  // the bins of the targets, with bounds where a target is not known yet
+  const double p = (double)g.top_p, u = (double)g.u;
+  const uint32_t k1 = g.top_k > 0 && (uint32_t)g.top_k < live ? (uint32_t)g.top_k : live;
+  const bool cut_k = k1 < near, cut_p = g.top_p < 1.0f;
+  Wanted want;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    want.lo[i] = kBins;
+    want.hi[i] = -1;
+  }
+  double m_lo = total, m_hi = total;
+  uint32_t k_hi = k1;
+  if (cut_k) {
+    const int b = bin_of<THREADS>(s, Target{kCount, k1, 0.0}, near);
+    want.lo[0] = want.hi[0] = b;
+    m_lo = mass_before(b);
+    m_hi = s.cum[b];
+  }
+  if (cut_p) {
+    want.hi[1] = bin_of<THREADS>(s, Target{kReach, 0, p * m_hi}, near);
+    want.lo[1] = cut_k ? bin_of<THREADS>(s, Target{kReach, 0, p * m_lo}, near) : want.hi[1];
+    m_lo = fmin(m_lo, mass_before(want.lo[1]));
+    m_hi = fmin(m_hi, s.cum[want.hi[1]]);
+    k_hi = k_hi < s.num[want.hi[1]] ? k_hi : s.num[want.hi[1]];
+  }
+  const bool cut_m = all.min < k_hi && all.min < near;
+  const Cuts cuts{p, u, total, k1, all.min, near, cut_k, cut_p, cut_m};
+  if (cut_m) {
+    const int b = bin_of<THREADS>(s, Target{kCount, all.min, 0.0}, near);
+    want.lo[2] = want.hi[2] = b;
+    m_lo = fmin(m_lo, mass_before(b));
+    m_hi = fmin(m_hi, s.cum[b]);
+  }
+  want.hi[3] = bin_of<THREADS>(s, Target{kExceed, 0, u * m_hi}, near);
+  want.lo[3] = m_lo < m_hi ? bin_of<THREADS>(s, Target{kExceed, 0, u * m_lo}, near) : want.hi[3];
+
+  uint32_t n_want = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int b = (int)threadIdx.x * kPer + i;
+    if (want.has(b)) n_want += s.num[b] - num_before(b);
+  }
+  n_want = reduce<THREADS>(n_want, s.wave_u, Add());
+
   uint32_t kept = k1;
-  double M = m1;
-  if (top_p < 1.0f) {
-    const Place p = find(Target{kReach, 0, (double)top_p * m1}, false);
-    if (p.rank < kept) {
-      kept = p.rank;
-      M = p.mass;
+  double M = total;
+  Place at;
+  if (__builtin_expect(n_want <= (uint32_t)kList, 1)) {
+    // gather: a band of logits (widened by more than its roundings) first, then the bin
+    int b_lo = want.lo[3], b_hi = want.hi[3];
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      b_lo = want.lo[i] < b_lo ? want.lo[i] : b_lo;
+      b_hi = want.hi[i] > b_hi ? want.hi[i] : b_hi;
     }
+    const double z_hi = (c.c - (double)b_lo) / c.l64, z_lo = (c.c - (double)(b_hi + 1)) / c.l64;
+    const double slack = fabs(c.c / c.l64) * 0x1p-40 + 1e-37;
+    const float top = (float)(z_hi + fabs(z_hi) * 0x1p-22 + slack);
+    const float end = (float)(z_lo - fabs(z_lo) * 0x1p-22 - slack);
+    for_each<THREADS, 8>(r, 0, r.n_vec, [&](float z, int i) {
+      if (z >= end && z <= top && z > -INFINITY) {
+        const double X = x_of(z, c);
+        if (X < kFar && want.has((int)X)) {
+          const uint32_t to = atomicAdd(&s.n_list, 1u);
+          if (to < (uint32_t)kList) s.list[to] = (u64)(~key_of(z)) << 32 | (uint32_t)i;
+        }
+      }
+    });
+    __syncthreads();
+    const int n = s.n_list < (uint32_t)kList ? (int)s.n_list : kList;
+    sort_list<THREADS>(s, n);
+    // each thread's tokens: the cumulative mass and number of the whole order at each,
+    // from sums that start anew with every bin
+    double mass[kMine];
+    uint32_t rank[kMine];
+    u64 q[kMine];
+    int bin[kMine];
+    const int first = (int)threadIdx.x * kMine;
+    auto entry_bin = [&](int i) { return (int)x_of(value_of(~(uint32_t)(s.list[i] >> 32)), c); };
+    u64 sum = 0;
+    uint32_t run = 0;          // tokens of the last bin so far, of which `sum`
+    bool head = false;         // whether a bin starts here
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      if (first + i < n) {
+        const double X = x_of(value_of(~(uint32_t)(s.list[first + i] >> 32)), c);
+        bin[i] = (int)X;
+        const int prev = i ? bin[i - 1] : first > 0 ? entry_bin(first - 1) : -1;
+        if (bin[i] != prev) {
+          head = true;
+          sum = 0;
+          run = 0;
+        }
+        sum += weight_of(X - (double)bin[i], c);
+        ++run;
+        q[i] = sum;
+        rank[i] = head ? run : 0x80000000u | run;     // (marked: lacks what came before)
+      }
+    }
+    // sums of the bins that began in earlier threads: a scan that restarts at heads
+    u64 in_sum = sum;
+    uint32_t in_run = run | (head ? 0x80000000u : 0u);
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const u64 o_sum = __shfl_up(in_sum, off);
+      const uint32_t o_run = __shfl_up(in_run, off);
+      if ((int)(threadIdx.x % 64) >= off && !(in_run & 0x80000000u)) {
+        in_sum += o_sum;
+        in_run += o_run;       // (takes the mark over)
+      }
+    }
+    if (threadIdx.x % 64 == 63) {
+      s.wave_q[threadIdx.x / 64] = in_sum;
+      s.wave_u[threadIdx.x / 64] = in_run;
+    }
+    __syncthreads();
+    u64 w_sum = 0;
+    uint32_t w_run = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w)
+      if (w < (int)(threadIdx.x / 64)) {
+        const bool anew = (s.wave_u[w] & 0x80000000u) != 0;
+        w_sum = (anew ? 0 : w_sum) + s.wave_q[w];
+        w_run = (anew ? 0 : w_run) + (s.wave_u[w] & 0x7FFFFFFFu);
+      }
+    u64 e_sum = __shfl_up(in_sum, 1);
+    uint32_t e_run = __shfl_up(in_run, 1);
+    if (threadIdx.x % 64 == 0) {
+      e_sum = w_sum;
+      e_run = w_run;
+    } else if (!(e_run & 0x80000000u)) {
+      e_sum += w_sum;
+      e_run += w_run;
+    }
+    e_run &= 0x7FFFFFFFu;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      if (first + i < n) {
+        if (rank[i] & 0x80000000u) {
+          q[i] += e_sum;
+          rank[i] = (rank[i] & 0x7FFFFFFFu) + e_run;
+        }
+        const int b = bin[i];
+        rank[i] += num_before(b);
+        // (the bin's last token has the bin's cumulative mass to the last bit)
+        mass[i] = rank[i] == s.num[b] ? s.cum[b]
+                                      : fmin(s.cum[b], mass_before(b) + step_of(b, c) * (double)q[i]);
+      } else {
+        rank[i] = 0xFFFFFFFFu;
+        mass[i] = 0.0;
+      }
+    }
+    // the first rank that meets a target, and what stands there
+    auto resolve = [&](const Target& tg) {
+      uint32_t f = 0xFFFFFFFFu;
+#pragma unroll
+      for (int i = kMine - 1; i >= 0; --i)
+        if (rank[i] != 0xFFFFFFFFu && tg.met(mass[i], rank[i])) f = rank[i];
+      f = reduce<THREADS>(f, s.wave_u, [](uint32_t x, uint32_t y) { return x < y ? x : y; });
+#pragma unroll
+      for (int i = 0; i < kMine; ++i)
+        if (rank[i] == f && f != 0xFFFFFFFFu) {
+          s.at_mass[0] = mass[i];
+          s.at_key = ~(uint32_t)(s.list[first + i] >> 32);
+          s.at_index = (int)(uint32_t)s.list[first + i];
+        }
+      __syncthreads();
+      const Place x{s.at_mass[0], f, s.at_key, s.at_index};
+      __syncthreads();
+      return x;
+    };
+    if (cut_k) M = resolve(Target{kCount, k1, 0.0}).mass;
+    if (cut_p) {
+      const Place x = resolve(Target{kReach, 0, p * M});
+      if (x.rank < kept) {
+        kept = x.rank;
+        M = x.mass;
+      }
+    }
+    if (cut_m && all.min < kept) {
+      kept = all.min;
+      M = resolve(Target{kCount, kept, 0.0}).mass;
+    }
+    at = resolve(Target{kExceed, 0, u * M});
+  } else {
+    at = one_by_one<THREADS>(r, s, c, cuts, &kept, &M);
   }
-  if (n_min < kept) {       // (at least the largest logit passes min_p)
-    kept = n_min;
-    M = mass_of(kept);
+  if (all.min < kept) kept = all.min;        // (tokens past the bins that min_p drops)
+  const double lw = -x_of(value_of(at.key), c) * (0.69314718055994530942 / 64.0);
+  return Drawn{at.index, (float)(lw - log(total)), (float)(lw - log(M)), kept};
+}
+
+__device__ __forceinline__ void clear_bins(Lds& s, int threads) {
+  for (int i = (int)threadIdx.x; i < kBins; i += threads) {
+    s.mass[i] = 0;
+    s.num[i] = 0;
   }
-  const Place p = find(Target{kExceed, 0, (double)u * M}, true);
-  const double lw = -x_of(value_of(p.key), c) * (0.69314718055994530942 / 64.0);
-  put(p.index, (float)(lw - log(total)), (float)(lw - log(M)), kept);
+}
+
+// ------------------------------------------------------------------ a work-group per row
+constexpr int kRowThreads = 512;
+
+template <bool F32>
+__global__ __launch_bounds__(kRowThreads, 4) void sample_rows_kernel(SampleArgs a, int64_t t0,
+                                                                     double unit) {
+  __shared__ Lds s;
+  const int64_t t = t0 + blockIdx.x;
+  const Settings g = settings_of(a, t);
+  if (g.left_out) return put(a, t, left_out());
+  if (!g.legal) return put(a, t, no_token());
+  const Row<F32> r = row_of<F32>(a, t);
+  clear_bins(s, kRowThreads);
+  const float m = reduce<kRowThreads>(max_part<kRowThreads>(r, 0, r.n_vec),
+                                      reinterpret_cast<float*>(s.wave_u), max_or_nan);
+  if (!(fabsf(m) < INFINITY)) return put(a, t, no_token());
+  const Scale c = scale_of(m, g.tau, unit);
+  Counts n = bin_part<kRowThreads>(r, 0, r.n_vec, s, c, g.min_p);
+  n.far = reduce<kRowThreads>(n.far, s.wave_u, Add());
+  n.min = reduce<kRowThreads>(n.min, s.wave_u, Add());
+  put(a, t, pick<kRowThreads>(r, s, c, g, n));
+}
+
+// ------------------------------------------------------------------ few rows, in pieces
+// Three launches: the pieces' largest logits; their bins, added to the row's in the
+// workspace; the token.
+constexpr int kPieceThreads = 512, kPickThreads = 1024;
+struct RowBins {
+  u64 mass[kBins];
+  uint32_t num[kBins];
+  uint32_t far, min;
+  uint32_t pad[62];
+};
+struct PieceArgs {
+  SampleArgs a;
+  double unit;
+  int pieces, vecs;     // of a row; 16-byte vectors of a piece
+  RowBins* rows;
+  float* max;           // [row][piece]
+};
+
+__device__ __forceinline__ float row_max(const PieceArgs& p, int64_t t) {
+  float m = -INFINITY;
+  for (int i = 0; i < p.pieces; ++i) m = max_or_nan(m, p.max[t * p.pieces + i]);
+  return m;
+}
+
+template <bool F32>
+__global__ __launch_bounds__(kPieceThreads) void piece_max_kernel(PieceArgs p) {
+  __shared__ float lds[kMaxWaves];
+  const int64_t t = blockIdx.x / p.pieces;
+  const int i = blockIdx.x % p.pieces;
+  // this piece's share of the row's bins, cleared for the next launch
+  uint32_t* const words = reinterpret_cast<uint32_t*>(p.rows + t);
+  constexpr int kWords = sizeof(RowBins) / 4;
+  const int share = (kWords + p.pieces - 1) / p.pieces;
+  for (int w = i * share + (int)threadIdx.x; w < kWords && w < (i + 1) * share; w += kPieceThreads)
+    words[w] = 0;
+  const Settings g = settings_of(p.a, t);
+  if (g.left_out || !g.legal) return;
+  const Row<F32> r = row_of<F32>(p.a, t);
+  const int64_t v0 = (int64_t)i * p.vecs, v1 = v0 + p.vecs < r.n_vec ? v0 + p.vecs : r.n_vec;
+  const float m = reduce<kPieceThreads>(max_part<kPieceThreads>(r, (int)v0, (int)v1), lds,
+                                        max_or_nan);
+  if (threadIdx.x == 0) p.max[blockIdx.x] = m;
+}
+
+template <bool F32>
+__global__ __launch_bounds__(kPieceThreads) void piece_bins_kernel(PieceArgs p) {
+  __shared__ Lds s;
+  const int64_t t = blockIdx.x / p.pieces;
+  const int i = blockIdx.x % p.pieces;
+  const Settings g = settings_of(p.a, t);
+  if (g.left_out || !g.legal) return;
+  const float m = row_max(p, t);
+  if (!(fabsf(m) < INFINITY)) return;
+  clear_bins(s, kPieceThreads);
+  __syncthreads();
+  const Row<F32> r = row_of<F32>(p.a, t);
+  const Scale c = scale_of(m, g.tau, p.unit);
+  const int64_t v0 = (int64_t)i * p.vecs, v1 = v0 + p.vecs < r.n_vec ? v0 + p.vecs : r.n_vec;
+  Counts n = bin_part<kPieceThreads>(r, (int)v0, (int)v1, s, c, g.min_p);
+  n.far = reduce<kPieceThreads>(n.far, s.wave_u, Add());
+  n.min = reduce<kPieceThreads>(n.min, s.wave_u, Add());
+  RowBins& to = p.rows[t];
+  for (int b = (int)threadIdx.x; b < kBins; b += kPieceThreads)
+    if (s.num[b] != 0) {
+      atomicAdd(&to.mass[b], s.mass[b]);
+      atomicAdd(&to.num[b], s.num[b]);
+    }
+  if (threadIdx.x == 0) {
+    if (n.far) atomicAdd(&to.far, n.far);
+    if (n.min) atomicAdd(&to.min, n.min);
+  }
+}
+
+template <bool F32>
+__global__ __launch_bounds__(kPickThreads) void pick_kernel(PieceArgs p) {
+  __shared__ Lds s;
+  const int64_t t = blockIdx.x;
+  const Settings g = settings_of(p.a, t);
+  if (g.left_out) return put(p.a, t, left_out());
+  const float m = g.legal ? row_max(p, t) : NAN;
+  if (!(fabsf(m) < INFINITY)) return put(p.a, t, no_token());
+  const RowBins& from = p.rows[t];
+  for (int b = (int)threadIdx.x; b < kBins; b += kPickThreads) {
+    s.mass[b] = from.mass[b];
+    s.num[b] = from.num[b];
+  }
+  const Counts n{from.far, from.min};
+  __syncthreads();
+  put(p.a, t, pick<kPickThreads>(row_of<F32>(p.a, t), s, scale_of(m, g.tau, p.unit), g, n));
+}
+
+// Pieces of a row: about two work-groups a CU in all, of at least 1024 vectors (a
+// piece's bins cost it about as much as these); one: a work-group per row.
+int pieces_of(int64_t n_tok, int64_t vocab) {
+  const int64_t vecs = vocab / 8;
+  int64_t most = vecs / 512, want = 256 / (n_tok > 0 ? n_tok : 1);
+  if (want > most) want = most;
+  if (want > 64) want = 64;
+  return want < 2 ? 1 : (int)want;
 }
 
 }  // namespace
 
-size_t sample_ws_bytes(int64_t, int64_t) { return 0; }
+size_t sample_ws_bytes(int64_t n_tok, int64_t vocab) {
+  const int pieces = pieces_of(n_tok, vocab);
+  if (n_tok == 0 || pieces == 1) return 0;
+  return (size_t)n_tok * sizeof(RowBins) + (size_t)round_up(n_tok * pieces * 4, 256);
+}
 
-hipError_t launch_sample(const SampleArgs& a, bool f32, char*, hipStream_t s) {
+hipError_t launch_sample(const SampleArgs& a, bool f32, char* ws, hipStream_t s) {
   // a bin's sum of `vocab` integers up to 2^bits stays below 2^63
   int bits = 45;
   while (bits > 32 && ((double)a.vocab * exp2((double)bits)) > 0x1p63) --bits;
   const double unit = exp2((double)bits);
-  auto kernel = f32 ? sample_kernel<true> : sample_kernel<false>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)a.n_tok), dim3(kThreads), 0, s, a, unit);
+  const int pieces = pieces_of(a.n_tok, a.vocab);
+  if (pieces == 1) {
+    auto kernel = f32 ? sample_rows_kernel<true> : sample_rows_kernel<false>;
+    constexpr int64_t kMost = 1 << 22;      // rows of a launch (2^31 threads)
+    for (int64_t t = 0; t < a.n_tok; t += kMost)
+      hipLaunchKernelGGL(kernel, dim3((unsigned)(a.n_tok - t < kMost ? a.n_tok - t : kMost)),
+                         dim3(kRowThreads), 0, s, a, t, unit);
+    return hipGetLastError();
+  }
+  const int e = f32 ? 4 : 8;
+  const int64_t n_vec = ((int64_t)a.vocab + e - 1) / e;
+  PieceArgs p{a, unit, pieces, (int)((n_vec + pieces - 1) / pieces),
+              reinterpret_cast<RowBins*>(ws),
+              reinterpret_cast<float*>(ws + (size_t)a.n_tok * sizeof(RowBins))};
+  const dim3 grid((unsigned)(a.n_tok * pieces));
+  if (f32) {
+    hipLaunchKernelGGL(piece_max_kernel<true>, grid, dim3(kPieceThreads), 0, s, p);
+    hipLaunchKernelGGL(piece_bins_kernel<true>, grid, dim3(kPieceThreads), 0, s, p);
+    hipLaunchKernelGGL(pick_kernel<true>, dim3((unsigned)a.n_tok), dim3(kPickThreads), 0, s, p);
+  } else {
+    hipLaunchKernelGGL(piece_max_kernel<false>, grid, dim3(kPieceThreads), 0, s, p);
+    hipLaunchKernelGGL(piece_bins_kernel<false>, grid, dim3(kPieceThreads), 0, s, p);
+    hipLaunchKernelGGL(pick_kernel<false>, dim3((unsigned)a.n_tok), dim3(kPickThreads), 0, s, p);
+  }
   return hipGetLastError();
 }
 
