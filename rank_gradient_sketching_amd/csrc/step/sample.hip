@@ -96,37 +96,44 @@ __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key ^ ((key & 0x80000000u) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-// What a row's weights are formed with.  X = z (-l64) + m l64 in one fused step: the
-// rounding of m l64 is common to all tokens and cancels in every ratio of masses (x0,
-// the largest logit's own X, is that rounding).
+// What a row's weights are formed with.  w: the polynomial's coefficients times 2^bits,
+// bits of a weight's integer, and on the last one 2^52, which leaves the rounded integer
+// in the low bits of the mantissa.
 struct Scale {
-  double l64, c, x0;  // 64 log2(e) / tau, m l64
-  double unit;        // 2^bits, bits of a weight's integer
+  double m, l64;      // largest logit, 64 log2(e) / tau
+  double w[6];
+  double unit;        // 2^bits
 };
 __device__ __forceinline__ Scale scale_of(float m, float tau, double unit) {
+  constexpr double t = -0.010830424696249145;      // -ln(2) / 64
+  constexpr double c1 = t, c2 = c1 * t / 2, c3 = c2 * t / 3, c4 = c3 * t / 4, c5 = c4 * t / 5;
   Scale s;
   s.l64 = 64.0 * 1.4426950408889634074 / (double)tau;
-  s.c = (double)m * s.l64;
-  s.x0 = fma((double)m, -s.l64, s.c);
+  s.m = (double)m;
+  s.w[0] = unit + 0x1p52;
+  s.w[1] = c1 * unit;
+  s.w[2] = c2 * unit;
+  s.w[3] = c3 * unit;
+  s.w[4] = c4 * unit;
+  s.w[5] = c5 * unit;
   s.unit = unit;
   return s;
 }
 __device__ __forceinline__ double x_of(float z, const Scale& s) {
-  return fma((double)z, -s.l64, s.c) - s.x0;
+  return (s.m - (double)z) * s.l64;
 }
 
-// round(2^(-r / 64) unit) for r in [0, 1): the series of e^t, t = -r ln(2) / 64.
-__device__ __forceinline__ u64 weight_of(double r, const Scale& c) {
-  constexpr double t = -0.010830424696249145;      // -ln(2) / 64
-  constexpr double c1 = t, c2 = c1 * t / 2, c3 = c2 * t / 3, c4 = c3 * t / 4, c5 = c4 * t / 5;
-  double p = fma(c5, r, c4);
-  p = fma(p, r, c3);
-  p = fma(p, r, c2);
-  p = fma(p, r, c1);
-  p = fma(p, r, 1.0);
-  // adding 2^52 leaves the rounded integer in the low bits of the mantissa
-  const double q = fma(p, c.unit, 0x1p52);
-  return (u64)__double_as_longlong(q) & 0xFFFFFFFFFFFFFull;
+// round(2^(-frac(X) / 64) unit) + kBias, the pattern of 2^52: sums of these wrap round
+// 2^64, and n kBias taken off a sum of n leaves the sum of the integers.
+constexpr u64 kBias = 0x4330000000000000ull;
+__device__ __forceinline__ u64 weight_of(double X, const Scale& c) {
+  const double r = __builtin_amdgcn_fract(X);
+  double p = fma(c.w[5], r, c.w[4]);
+  p = fma(p, r, c.w[3]);
+  p = fma(p, r, c.w[2]);
+  p = fma(p, r, c.w[1]);
+  p = fma(p, r, c.w[0]);
+  return (u64)__double_as_longlong(p);
 }
 // What an integer of bin b stands for.
 __device__ __forceinline__ double step_of(int b, const Scale& c) {
@@ -141,6 +148,8 @@ struct Lds {
     double cum[kBins];       // then: cumulative masses
   };
   uint32_t num[kBins];       // numbers of tokens, then cumulative
+  double group_cum[64];      // of every 64th bin
+  uint32_t group_num[64];
   union {
     u64 list[kList];         // ~key, index
     struct {
@@ -153,8 +162,8 @@ struct Lds {
     u64 wave_q[kMaxWaves];
   };
   uint32_t wave_u[kMaxWaves];
-  double at_mass[2];
-  uint32_t at_rank[2], at_key, n_list;
+  double at_mass;
+  uint32_t at_rank, at_key, n_list;
   int at_index;
 };
 
@@ -301,7 +310,7 @@ __device__ __noinline__ Place refine(Row<F32> r, Lds& s, Scale c, int b, Target 
       const uint32_t k = key_of(z);
       if (X < kFar && (int)X == b && k >= lo && k <= hi) {
         const uint32_t sub = (hi - k) >> shift;
-        atomicAdd(&s.sub.mass[sub], weight_of(X - (double)b, c));
+        atomicAdd(&s.sub.mass[sub], weight_of(X, c) - kBias);
         atomicAdd(&s.sub.num[sub], 1u);
       }
     });
@@ -367,16 +376,17 @@ struct Cuts {
   uint32_t k1, min, near;      // near: tokens in the bins
   bool k, by_p, by_min;        // which cuts there are
 };
-// The bin where the order meets a target.
-template <int THREADS>
-__device__ __forceinline__ int bin_of(Lds& s, const Target& t, uint32_t near) {
-  auto bins = [&](int b, double* x, uint32_t* n) {
-    *x = s.cum[b];
-    *n = s.num[b];
-  };
-  const int b = first_met<THREADS, kBins>(s, t, bins);
+// The bin where the order meets a target: every wave finds it for itself, first the 64
+// bins that hold it, then the one.
+__device__ __forceinline__ int bin_of(const Lds& s, const Target& t, uint32_t near) {
+  const int lane = threadIdx.x & 63;
+  u64 met = __ballot(t.met(s.group_cum[lane], s.group_num[lane]));
   // (unmet by a rounding: the last bin that holds a token)
-  return b >= 0 ? b : first_met<THREADS, kBins>(s, Target{kCount, near, 0.0}, bins);
+  const Target last{kCount, near, 0.0};
+  const Target& u = met ? t : last;
+  if (met == 0) met = __ballot(u.met(s.group_cum[lane], s.group_num[lane]));
+  const int g = (__ffsll(met) - 1) * 64;
+  return g + __ffsll(__ballot(u.met(s.cum[g + lane], s.num[g + lane]))) - 1;
 }
 template <int THREADS, bool F32>
 __device__ __noinline__ Place one_by_one(Row<F32> r, Lds& s, Scale c, Cuts x, uint32_t* kept,
@@ -397,7 +407,7 @@ __device__ __noinline__ Place one_by_one(Row<F32> r, Lds& s, Scale c, Cuts x, ui
       t.count = x.min;
     }
     if (i == 3) t = Target{kExceed, 0, x.u * m};
-    at = refine<THREADS>(r, s, c, bin_of<THREADS>(s, t, x.near), t, i == 3);
+    at = refine<THREADS>(r, s, c, bin_of(s, t, x.near), t, i == 3);
     if (i == 0 || (i < 3 && at.rank < k)) {
       k = at.rank;
       m = at.mass;
@@ -464,29 +474,39 @@ __device__ __forceinline__ float max_or_nan(float a, float b) {
   return a != a ? a : b != b ? b : fmaxf(a, b);
 }
 
-// Tokens that only count, and those that pass min_p.
+// Tokens that only count, and those that pass min_p (without it: kAll).
+constexpr uint32_t kAll = 0xFFFFFFFFu;
 struct Counts {
   uint32_t far, min;
 };
 // Fills the bins with the logits of vectors [v0, v1); a thread's own Counts.
-template <int THREADS, bool F32>
+template <int THREADS, bool MIN, bool F32>
 __device__ __forceinline__ Counts bin_part(const Row<F32>& r, int v0, int v1, Lds& s,
-                                           const Scale& c, float min_p) {
+                                           const Scale& c, double x_min) {
   Counts n{0, 0};
-  const double x_min = min_p > 0.0f ? -64.0 * log2((double)min_p) : INFINITY;
   for_each<THREADS, 4>(r, v0, v1, [&](float z, int) {
-    if (z > -INFINITY) {
-      const double X = x_of(z, c);
-      n.min += X <= x_min;
-      if (X < kFar) {
-        const int b = (int)X;
-        atomicAdd(&s.mass[b], weight_of(X - (double)b, c));
-        atomicAdd(&s.num[b], 1u);
-      } else {
-        ++n.far;
-      }
+    const double X = x_of(z, c);
+    if constexpr (MIN) n.min += X <= x_min;
+    if (X < kFar) {
+      const int b = (int)X;
+      atomicAdd(&s.mass[b], weight_of(X, c));
+      atomicAdd(&s.num[b], 1u);
+    } else if (z > -INFINITY) {
+      ++n.far;
     }
   });
+  return n;
+}
+template <int THREADS, bool F32>
+__device__ __forceinline__ Counts fill_bins(const Row<F32>& r, int v0, int v1, Lds& s,
+                                            const Scale& c, float min_p) {
+  Counts n;
+  if (min_p > 0.0f)
+    n = bin_part<THREADS, true>(r, v0, v1, s, c, -64.0 * log2((double)min_p));
+  else
+    n = bin_part<THREADS, false>(r, v0, v1, s, c, 0.0);
+  n.far = reduce<THREADS>(n.far, s.wave_u, Add());
+  n.min = min_p > 0.0f ? reduce<THREADS>(n.min, s.wave_u, Add()) : kAll;
   return n;
 }
 
@@ -520,19 +540,248 @@ __device__ __forceinline__ void sort_list(Lds& s, int n) {
     }
 }
 
+// What a thread knows of one token of the sorted list.
+struct Entry {
+  double mass;        // cumulative, as is the rank; 0 where there is no token
+  uint32_t rank;
+};
+// The cumulative mass and number at a token of bin b that is the n-th of its bin, q the
+// sum of the bin's integers up to it.
+__device__ __forceinline__ Entry entry_of(const Lds& s, const Scale& c, int b, u64 q, uint32_t n) {
+  const double before = b > 0 ? s.cum[b - 1] : 0.0;
+  Entry e;
+  e.rank = (b > 0 ? s.num[b - 1] : 0u) + n;
+  // (the bin's last token has the bin's cumulative mass to the last bit)
+  e.mass = e.rank == s.num[b] ? s.cum[b] : fmin(s.cum[b], before + step_of(b, c) * (double)q);
+  return e;
+}
+// The kept number, their mass and the draw, from a function that resolves targets.
+template <class F>
+__device__ __forceinline__ Place resolve_all(const Cuts& x, uint32_t* kept, double* M, F resolve) {
+  if (x.k) *M = resolve(Target{kCount, x.k1, 0.0}).mass;
+  if (x.by_p) {
+    const Place at = resolve(Target{kReach, 0, x.p * *M});
+    if (at.rank < *kept) {
+      *kept = at.rank;
+      *M = at.mass;
+    }
+  }
+  if (x.by_min && x.min < *kept) {
+    *kept = x.min;
+    *M = resolve(Target{kCount, x.min, 0.0}).mass;
+  }
+  return resolve(Target{kExceed, 0, x.u * *M});
+}
+
+// A list of at most 64 tokens, one per lane: every wave sorts and resolves it for itself.
+__device__ __forceinline__ Place resolve_short(const Lds& s, const Scale& c, const Cuts& x, int n,
+                                               uint32_t* kept, double* M) {
+  const int lane = threadIdx.x & 63;
+  const u64 mine = lane < n ? s.list[lane] : ~0ull;
+  int place = lane;                       // (lanes without a token stay behind)
+  if (lane < n) place = 0;
+  for (int i = 0; i < n; ++i) place += lane < n && s.list[i] < mine;
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_permute(place * 4, (int)(mine >> 32));
+  const uint32_t index = (uint32_t)__builtin_amdgcn_ds_permute(place * 4, (int)mine);
+  const uint32_t key = ~hi;
+  const double X = x_of(value_of(key), c);
+  const int b = lane < n ? (int)X : -1;
+  u64 q = lane < n ? weight_of(X, c) - kBias : 0;
+  uint32_t run = 1;
+  const int b_before = __shfl_up(b, 1);       // (every lane takes part)
+  bool head = lane == 0 || b != b_before;
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const u64 o_q = __shfl_up(q, off);
+    const uint32_t o_run = __shfl_up(run, off);
+    const bool o_head = __shfl_up((int)head, off) != 0;
+    if (lane >= off && !head) {
+      q += o_q;
+      run += o_run;
+      head = o_head;
+    }
+  }
+  Entry e{0.0, 0};
+  if (lane < n) e = entry_of(s, c, b, q, run);
+  return resolve_all(x, kept, M, [&](const Target& t) {
+    const u64 met = __ballot(lane < n && t.met(e.mass, e.rank));
+    const int f = met ? __ffsll(met) - 1 : n - 1;
+    return Place{__shfl(e.mass, f), (uint32_t)__shfl((int)e.rank, f), (uint32_t)__shfl((int)key, f),
+                 __shfl((int)index, f)};
+  });
+}
+
+// A longer list: sorted in LDS, kList / THREADS consecutive tokens a thread.
+template <int THREADS>
+__device__ __noinline__ Place resolve_long(Lds& s, Scale c, Cuts x, int n, uint32_t* kept,
+                                           double* M) {
+  constexpr int kMine = kList / THREADS;
+  sort_list<THREADS>(s, n);
+  // sums of a bin's integers and tokens up to each token, which start anew with every bin
+  u64 q[kMine];
+  uint32_t run[kMine];
+  int bin[kMine];
+  const int first = (int)threadIdx.x * kMine;
+  auto x_at = [&](int i) { return x_of(value_of(~(uint32_t)(s.list[i] >> 32)), c); };
+  u64 sum = 0;
+  uint32_t ns = 0;
+  bool head = false;         // whether a bin starts here
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    if (first + i < n) {
+      const double X = x_at(first + i);
+      bin[i] = (int)X;
+      const int prev = i ? bin[i - 1] : first > 0 ? (int)x_at(first - 1) : -1;
+      if (bin[i] != prev) {
+        head = true;
+        sum = 0;
+        ns = 0;
+      }
+      sum += weight_of(X, c) - kBias;
+      ++ns;
+      q[i] = sum;
+      run[i] = head ? ns : 0x80000000u | ns;     // (marked: lacks what came before)
+    }
+  }
+  // sums of the bins that began in earlier threads: a scan that restarts at heads
+  u64 in_sum = sum;
+  uint32_t in_run = ns | (head ? 0x80000000u : 0u);
+#pragma unroll
+  for (int off = 1; off < 64; off <<= 1) {
+    const u64 o_sum = __shfl_up(in_sum, off);
+    const uint32_t o_run = __shfl_up(in_run, off);
+    if ((int)(threadIdx.x % 64) >= off && !(in_run & 0x80000000u)) {
+      in_sum += o_sum;
+      in_run += o_run;       // (takes the mark over)
+    }
+  }
+  if (threadIdx.x % 64 == 63) {
+    s.wave_q[threadIdx.x / 64] = in_sum;
+    s.wave_u[threadIdx.x / 64] = in_run;
+  }
+  __syncthreads();
+  u64 w_sum = 0;
+  uint32_t w_run = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 64; ++w)
+    if (w < (int)(threadIdx.x / 64)) {
+      const bool anew = (s.wave_u[w] & 0x80000000u) != 0;
+      w_sum = (anew ? 0 : w_sum) + s.wave_q[w];
+      w_run = (anew ? 0 : w_run) + (s.wave_u[w] & 0x7FFFFFFFu);
+    }
+  __syncthreads();
+  u64 e_sum = __shfl_up(in_sum, 1);
+  uint32_t e_run = __shfl_up(in_run, 1);
+  if (threadIdx.x % 64 == 0) {
+    e_sum = w_sum;
+    e_run = w_run;
+  } else if (!(e_run & 0x80000000u)) {
+    e_sum += w_sum;
+    e_run += w_run;
+  }
+  e_run &= 0x7FFFFFFFu;
+  Entry e[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    e[i] = Entry{0.0, 0};
+    if (first + i < n) {
+      const bool lacks = (run[i] & 0x80000000u) != 0;
+      e[i] = entry_of(s, c, bin[i], q[i] + (lacks ? e_sum : 0),
+                      (run[i] & 0x7FFFFFFFu) + (lacks ? e_run : 0));
+    }
+  }
+  // the first rank that meets a target, and what stands there
+  return resolve_all(x, kept, M, [&](const Target& t) {
+    uint32_t f = 0xFFFFFFFFu;
+#pragma unroll
+    for (int i = kMine - 1; i >= 0; --i)
+      if (first + i < n && t.met(e[i].mass, e[i].rank)) f = e[i].rank;
+    f = reduce<THREADS>(f, s.wave_u, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+#pragma unroll
+    for (int i = 0; i < kMine; ++i)
+      if (first + i < n && (e[i].rank == f || (f == 0xFFFFFFFFu && first + i == n - 1))) {
+        s.at_mass = e[i].mass;
+        s.at_rank = e[i].rank;
+        s.at_key = ~(uint32_t)(s.list[first + i] >> 32);
+        s.at_index = (int)(uint32_t)s.list[first + i];
+      }
+    __syncthreads();
+    const Place at{s.at_mass, s.at_rank, s.at_key, s.at_index};
+    __syncthreads();
+    return at;
+  });
+}
+
+// A band of logits that holds a run of bins, widened by more than its roundings.
+struct Band {
+  float end, top;
+  __device__ __forceinline__ bool has(float z) const { return z >= end && z <= top; }
+};
+__device__ __forceinline__ Band band_of(int lo, int hi, const Scale& c) {
+  if (hi < lo) return Band{INFINITY, -INFINITY};
+  const double slack = fabs(c.m) * 0x1p-40 + 1e-37;
+  const double top = c.m - (double)lo / c.l64, end = c.m - (double)(hi + 1) / c.l64;
+  return Band{(float)(end - fabs(end) * 0x1p-22 - slack),
+              (float)(top + fabs(top) * 0x1p-22 + slack)};
+}
+// Puts the row's tokens of the wanted bins on the list.  Most groups of neighbours have
+// no logit as large as the lowest band's end.
+template <int THREADS, int BANDS, bool F32>
+__device__ __forceinline__ void gather(const Row<F32>& r, Lds& s, const Scale& c,
+                                       const Wanted& want, const Band* band) {
+  constexpr int E = Row<F32>::kE, U = 8;
+  float least = band[0].end;
+#pragma unroll
+  for (int i = 1; i < BANDS; ++i) least = fminf(least, band[i].end);
+  for (int at = (int)threadIdx.x; at < r.n_vec; at += U * THREADS) {
+    u32x4 q[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int v = at + i * THREADS;
+      q[i] = r.p[v < r.n_vec ? v : at];
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int v = at + i * THREADS;
+      float z[E];
+      logits_of<F32>(q[i], v < r.n_vec ? v : at, r.V, z);
+      float m = z[0];
+#pragma unroll
+      for (int e = 1; e < E; ++e) m = fmaxf(m, z[e]);
+      if (m >= least && v < r.n_vec) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          bool in = band[0].has(z[e]);
+#pragma unroll
+          for (int k = 1; k < BANDS; ++k) in = in || band[k].has(z[e]);
+          if (in && z[e] > -INFINITY) {
+            const double X = x_of(z[e], c);
+            if (X < kFar && want.has((int)X)) {
+              const uint32_t to = atomicAdd(&s.n_list, 1u);
+              if (to < (uint32_t)kList) s.list[to] = (u64)(~key_of(z[e])) << 32 | (uint32_t)(v * E + e);
+            }
+          }
+        }
+      }
+    }
+  }
+}
+
 // From the filled bins to the token.
 template <int THREADS, bool F32>
 __device__ __noinline__ Drawn pick(Row<F32> r, Lds& s, Scale c, Settings g, Counts all) {
-  constexpr int kPer = kBins / THREADS, kMine = kList / THREADS;
+  constexpr int kPer = kBins / THREADS;
   {
     // cumulative masses and numbers
-    double d[kPer], ds = 0;
+    double d[kPer], ds = 0, step = step_of((int)threadIdx.x * kPer, c);
     uint32_t n[kPer], ns = 0;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int b = (int)threadIdx.x * kPer + i;
-      d[i] = ds += (double)s.mass[b] * step_of(b, c);
-      n[i] = ns += s.num[b];
+      const uint32_t k = s.num[b];
+      d[i] = ds += (double)(s.mass[b] - k * kBias) * step;
+      n[i] = ns += k;
+      step *= 0.9892280131939755;        // 2^(-1 / 64)
     }
     const double d0 = before_me<THREADS>(ds, s.wave_d);
     const uint32_t n0 = before_me<THREADS>(ns, s.wave_u);
@@ -540,6 +789,10 @@ __device__ __noinline__ Drawn pick(Row<F32> r, Lds& s, Scale c, Settings g, Coun
     for (int i = 0; i < kPer; ++i) {
       s.cum[threadIdx.x * kPer + i] = d0 + d[i];
       s.num[threadIdx.x * kPer + i] = n0 + n[i];
+    }
+    if (((int)threadIdx.x + 1) * kPer % 64 == 0) {
+      s.group_cum[threadIdx.x * kPer / 64] = d0 + d[kPer - 1];
+      s.group_num[threadIdx.x * kPer / 64] = n0 + n[kPer - 1];
     }
     if (threadIdx.x == 0) s.n_list = 0;
     __syncthreads();
@@ -562,177 +815,51 @@ __device__ __noinline__ Drawn pick(Row<F32> r, Lds& s, Scale c, Settings g, Coun
   double m_lo = total, m_hi = total;
   uint32_t k_hi = k1;
   if (cut_k) {
-    const int b = bin_of<THREADS>(s, Target{kCount, k1, 0.0}, near);
+    const int b = bin_of(s, Target{kCount, k1, 0.0}, near);
     want.lo[0] = want.hi[0] = b;
     m_lo = mass_before(b);
     m_hi = s.cum[b];
   }
   if (cut_p) {
-    want.hi[1] = bin_of<THREADS>(s, Target{kReach, 0, p * m_hi}, near);
-    want.lo[1] = cut_k ? bin_of<THREADS>(s, Target{kReach, 0, p * m_lo}, near) : want.hi[1];
+    want.hi[1] = bin_of(s, Target{kReach, 0, p * m_hi}, near);
+    want.lo[1] = cut_k ? bin_of(s, Target{kReach, 0, p * m_lo}, near) : want.hi[1];
     m_lo = fmin(m_lo, mass_before(want.lo[1]));
     m_hi = fmin(m_hi, s.cum[want.hi[1]]);
     k_hi = k_hi < s.num[want.hi[1]] ? k_hi : s.num[want.hi[1]];
   }
   const bool cut_m = all.min < k_hi && all.min < near;
-  const Cuts cuts{p, u, total, k1, all.min, near, cut_k, cut_p, cut_m};
   if (cut_m) {
-    const int b = bin_of<THREADS>(s, Target{kCount, all.min, 0.0}, near);
+    const int b = bin_of(s, Target{kCount, all.min, 0.0}, near);
     want.lo[2] = want.hi[2] = b;
     m_lo = fmin(m_lo, mass_before(b));
     m_hi = fmin(m_hi, s.cum[b]);
   }
-  want.hi[3] = bin_of<THREADS>(s, Target{kExceed, 0, u * m_hi}, near);
-  want.lo[3] = m_lo < m_hi ? bin_of<THREADS>(s, Target{kExceed, 0, u * m_lo}, near) : want.hi[3];
+  want.hi[3] = bin_of(s, Target{kExceed, 0, u * m_hi}, near);
+  want.lo[3] = m_lo < m_hi ? bin_of(s, Target{kExceed, 0, u * m_lo}, near) : want.hi[3];
+  const Cuts cuts{p, u, total, k1, all.min, near, cut_k, cut_p, cut_m};
 
-  uint32_t n_want = 0;
+  uint32_t n_want = 0;         // (a bin wanted twice counts twice)
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    const int b = (int)threadIdx.x * kPer + i;
-    if (want.has(b)) n_want += s.num[b] - num_before(b);
-  }
-  n_want = reduce<THREADS>(n_want, s.wave_u, Add());
+  for (int i = 0; i < 4; ++i)
+    if (want.hi[i] >= want.lo[i]) n_want += s.num[want.hi[i]] - num_before(want.lo[i]);
 
   uint32_t kept = k1;
   double M = total;
   Place at;
   if (__builtin_expect(n_want <= (uint32_t)kList, 1)) {
-    // gather: a band of logits (widened by more than its roundings) first, then the bin
-    int b_lo = want.lo[3], b_hi = want.hi[3];
+    Band band[4];
 #pragma unroll
-    for (int i = 0; i < 3; ++i) {
-      b_lo = want.lo[i] < b_lo ? want.lo[i] : b_lo;
-      b_hi = want.hi[i] > b_hi ? want.hi[i] : b_hi;
-    }
-    const double z_hi = (c.c - (double)b_lo) / c.l64, z_lo = (c.c - (double)(b_hi + 1)) / c.l64;
-    const double slack = fabs(c.c / c.l64) * 0x1p-40 + 1e-37;
-    const float top = (float)(z_hi + fabs(z_hi) * 0x1p-22 + slack);
-    const float end = (float)(z_lo - fabs(z_lo) * 0x1p-22 - slack);
-    for_each<THREADS, 8>(r, 0, r.n_vec, [&](float z, int i) {
-      if (z >= end && z <= top && z > -INFINITY) {
-        const double X = x_of(z, c);
-        if (X < kFar && want.has((int)X)) {
-          const uint32_t to = atomicAdd(&s.n_list, 1u);
-          if (to < (uint32_t)kList) s.list[to] = (u64)(~key_of(z)) << 32 | (uint32_t)i;
-        }
-      }
-    });
+    for (int i = 0; i < 4; ++i) band[i] = band_of(want.lo[3 - i], want.hi[3 - i], c);
+    if (cut_k || cut_p || cut_m)
+      gather<THREADS, 4>(r, s, c, want, band);
+    else
+      gather<THREADS, 1>(r, s, c, want, band);
     __syncthreads();
     const int n = s.n_list < (uint32_t)kList ? (int)s.n_list : kList;
-    sort_list<THREADS>(s, n);
-    // each thread's tokens: the cumulative mass and number of the whole order at each,
-    // from sums that start anew with every bin
-    double mass[kMine];
-    uint32_t rank[kMine];
-    u64 q[kMine];
-    int bin[kMine];
-    const int first = (int)threadIdx.x * kMine;
-    auto entry_bin = [&](int i) { return (int)x_of(value_of(~(uint32_t)(s.list[i] >> 32)), c); };
-    u64 sum = 0;
-    uint32_t run = 0;          // tokens of the last bin so far, of which `sum`
-    bool head = false;         // whether a bin starts here
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      if (first + i < n) {
-        const double X = x_of(value_of(~(uint32_t)(s.list[first + i] >> 32)), c);
-        bin[i] = (int)X;
-        const int prev = i ? bin[i - 1] : first > 0 ? entry_bin(first - 1) : -1;
-        if (bin[i] != prev) {
-          head = true;
-          sum = 0;
-          run = 0;
-        }
-        sum += weight_of(X - (double)bin[i], c);
-        ++run;
-        q[i] = sum;
-        rank[i] = head ? run : 0x80000000u | run;     // (marked: lacks what came before)
-      }
-    }
-    // sums of the bins that began in earlier threads: a scan that restarts at heads
-    u64 in_sum = sum;
-    uint32_t in_run = run | (head ? 0x80000000u : 0u);
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const u64 o_sum = __shfl_up(in_sum, off);
-      const uint32_t o_run = __shfl_up(in_run, off);
-      if ((int)(threadIdx.x % 64) >= off && !(in_run & 0x80000000u)) {
-        in_sum += o_sum;
-        in_run += o_run;       // (takes the mark over)
-      }
-    }
-    if (threadIdx.x % 64 == 63) {
-      s.wave_q[threadIdx.x / 64] = in_sum;
-      s.wave_u[threadIdx.x / 64] = in_run;
-    }
-    __syncthreads();
-    u64 w_sum = 0;
-    uint32_t w_run = 0;
-#pragma unroll
-    for (int w = 0; w < THREADS / 64; ++w)
-      if (w < (int)(threadIdx.x / 64)) {
-        const bool anew = (s.wave_u[w] & 0x80000000u) != 0;
-        w_sum = (anew ? 0 : w_sum) + s.wave_q[w];
-        w_run = (anew ? 0 : w_run) + (s.wave_u[w] & 0x7FFFFFFFu);
-      }
-    u64 e_sum = __shfl_up(in_sum, 1);
-    uint32_t e_run = __shfl_up(in_run, 1);
-    if (threadIdx.x % 64 == 0) {
-      e_sum = w_sum;
-      e_run = w_run;
-    } else if (!(e_run & 0x80000000u)) {
-      e_sum += w_sum;
-      e_run += w_run;
-    }
-    e_run &= 0x7FFFFFFFu;
-#pragma unroll
-    for (int i = 0; i < kMine; ++i) {
-      if (first + i < n) {
-        if (rank[i] & 0x80000000u) {
-          q[i] += e_sum;
-          rank[i] = (rank[i] & 0x7FFFFFFFu) + e_run;
-        }
-        const int b = bin[i];
-        rank[i] += num_before(b);
-        // (the bin's last token has the bin's cumulative mass to the last bit)
-        mass[i] = rank[i] == s.num[b] ? s.cum[b]
-                                      : fmin(s.cum[b], mass_before(b) + step_of(b, c) * (double)q[i]);
-      } else {
-        rank[i] = 0xFFFFFFFFu;
-        mass[i] = 0.0;
-      }
-    }
-    // the first rank that meets a target, and what stands there
-    auto resolve = [&](const Target& tg) {
-      uint32_t f = 0xFFFFFFFFu;
-#pragma unroll
-      for (int i = kMine - 1; i >= 0; --i)
-        if (rank[i] != 0xFFFFFFFFu && tg.met(mass[i], rank[i])) f = rank[i];
-      f = reduce<THREADS>(f, s.wave_u, [](uint32_t x, uint32_t y) { return x < y ? x : y; });
-#pragma unroll
-      for (int i = 0; i < kMine; ++i)
-        if (rank[i] == f && f != 0xFFFFFFFFu) {
-          s.at_mass[0] = mass[i];
-          s.at_key = ~(uint32_t)(s.list[first + i] >> 32);
-          s.at_index = (int)(uint32_t)s.list[first + i];
-        }
-      __syncthreads();
-      const Place x{s.at_mass[0], f, s.at_key, s.at_index};
-      __syncthreads();
-      return x;
-    };
-    if (cut_k) M = resolve(Target{kCount, k1, 0.0}).mass;
-    if (cut_p) {
-      const Place x = resolve(Target{kReach, 0, p * M});
-      if (x.rank < kept) {
-        kept = x.rank;
-        M = x.mass;
-      }
-    }
-    if (cut_m && all.min < kept) {
-      kept = all.min;
-      M = resolve(Target{kCount, kept, 0.0}).mass;
-    }
-    at = resolve(Target{kExceed, 0, u * M});
+    if (n <= 64)
+      at = resolve_short(s, c, cuts, n, &kept, &M);
+    else
+      at = resolve_long<THREADS>(s, c, cuts, n, &kept, &M);
   } else {
     at = one_by_one<THREADS>(r, s, c, cuts, &kept, &M);
   }
@@ -765,9 +892,7 @@ __global__ __launch_bounds__(kRowThreads, 4) void sample_rows_kernel(SampleArgs 
                                       reinterpret_cast<float*>(s.wave_u), max_or_nan);
   if (!(fabsf(m) < INFINITY)) return put(a, t, no_token());
   const Scale c = scale_of(m, g.tau, unit);
-  Counts n = bin_part<kRowThreads>(r, 0, r.n_vec, s, c, g.min_p);
-  n.far = reduce<kRowThreads>(n.far, s.wave_u, Add());
-  n.min = reduce<kRowThreads>(n.min, s.wave_u, Add());
+  const Counts n = fill_bins<kRowThreads>(r, 0, r.n_vec, s, c, g.min_p);
   put(a, t, pick<kRowThreads>(r, s, c, g, n));
 }
 
@@ -790,8 +915,11 @@ struct PieceArgs {
 };
 
 __device__ __forceinline__ float row_max(const PieceArgs& p, int64_t t) {
-  float m = -INFINITY;
-  for (int i = 0; i < p.pieces; ++i) m = max_or_nan(m, p.max[t * p.pieces + i]);
+  // (at most 64 pieces: one a lane)
+  const int lane = threadIdx.x & 63;
+  float m = p.max[t * p.pieces + (lane < p.pieces ? lane : 0)];
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) m = max_or_nan(m, __shfl_xor(m, off));
   return m;
 }
 
@@ -829,9 +957,7 @@ __global__ __launch_bounds__(kPieceThreads) void piece_bins_kernel(PieceArgs p) 
   const Row<F32> r = row_of<F32>(p.a, t);
   const Scale c = scale_of(m, g.tau, p.unit);
   const int64_t v0 = (int64_t)i * p.vecs, v1 = v0 + p.vecs < r.n_vec ? v0 + p.vecs : r.n_vec;
-  Counts n = bin_part<kPieceThreads>(r, (int)v0, (int)v1, s, c, g.min_p);
-  n.far = reduce<kPieceThreads>(n.far, s.wave_u, Add());
-  n.min = reduce<kPieceThreads>(n.min, s.wave_u, Add());
+  const Counts n = fill_bins<kPieceThreads>(r, (int)v0, (int)v1, s, c, g.min_p);
   RowBins& to = p.rows[t];
   for (int b = (int)threadIdx.x; b < kBins; b += kPieceThreads)
     if (s.num[b] != 0) {
@@ -840,7 +966,7 @@ __global__ __launch_bounds__(kPieceThreads) void piece_bins_kernel(PieceArgs p) 
     }
   if (threadIdx.x == 0) {
     if (n.far) atomicAdd(&to.far, n.far);
-    if (n.min) atomicAdd(&to.min, n.min);
+    if (n.min != kAll && n.min) atomicAdd(&to.min, n.min);
   }
 }
 
@@ -857,7 +983,7 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(PieceArgs p) {
     s.mass[b] = from.mass[b];
     s.num[b] = from.num[b];
   }
-  const Counts n{from.far, from.min};
+  const Counts n{from.far, g.min_p > 0.0f ? from.min : kAll};
   __syncthreads();
   put(p.a, t, pick<kPickThreads>(row_of<F32>(p.a, t), s, scale_of(m, g.tau, p.unit), g, n));
 }
