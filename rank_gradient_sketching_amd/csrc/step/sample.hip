@@ -513,6 +513,7 @@ __device__ __forceinline__ Counts fill_bins(const Row<F32>& r, int v0, int v1, L
 // Bins that hold what the targets need: single ones and runs.
 struct Wanted {
   int lo[4], hi[4];
+  __device__ __forceinline__ bool has_x(double X) const { return X < kFar && has((int)X); }
   __device__ __forceinline__ bool has(int b) const {
     return (b >= lo[0] && b <= hi[0]) || (b >= lo[1] && b <= hi[1]) ||
            (b >= lo[2] && b <= hi[2]) || (b >= lo[3] && b <= hi[3]);
@@ -574,13 +575,21 @@ __device__ __forceinline__ Place resolve_all(const Cuts& x, uint32_t* kept, doub
 }
 
 // A list of at most 64 tokens, one per lane: every wave sorts and resolves it for itself.
-__device__ __forceinline__ Place resolve_short(const Lds& s, const Scale& c, const Cuts& x, int n,
-                                               uint32_t* kept, double* M) {
+__device__ __forceinline__ Place resolve_short(Lds& s, const Scale& c, const Cuts& x,
+                                               const Wanted& want, int n_list, uint32_t* kept,
+                                               double* M) {
   const int lane = threadIdx.x & 63;
-  const u64 mine = lane < n ? s.list[lane] : ~0ull;
-  int place = lane;                       // (lanes without a token stay behind)
-  if (lane < n) place = 0;
-  for (int i = 0; i < n; ++i) place += lane < n && s.list[i] < mine;
+  // (a neighbour of the wanted bins gets an entry past all others, as lanes without one)
+  u64 mine = lane < n_list ? s.list[lane] : ~0ull;
+  if (lane < n_list && !want.has_x(x_of(value_of(~(uint32_t)(mine >> 32)), c))) {
+    mine = ~0ull;
+    s.list[lane] = mine;
+  }
+  const u64 valid = __ballot(mine != ~0ull);
+  const int n = __popcll(valid);
+  int place = 0;
+  for (int i = 0; i < n_list; ++i) place += s.list[i] < mine;
+  if (mine == ~0ull) place = n + lane - __popcll(valid & ((1ull << lane) - 1));
   const uint32_t hi = (uint32_t)__builtin_amdgcn_ds_permute(place * 4, (int)(mine >> 32));
   const uint32_t index = (uint32_t)__builtin_amdgcn_ds_permute(place * 4, (int)mine);
   const uint32_t key = ~hi;
@@ -613,10 +622,20 @@ __device__ __forceinline__ Place resolve_short(const Lds& s, const Scale& c, con
 
 // A longer list: sorted in LDS, kList / THREADS consecutive tokens a thread.
 template <int THREADS>
-__device__ __noinline__ Place resolve_long(Lds& s, Scale c, Cuts x, int n, uint32_t* kept,
-                                           double* M) {
+__device__ __forceinline__ Place resolve_long(Lds& s, const Scale& c, const Cuts& x,
+                                              const Wanted& want, int n_list, uint32_t* kept,
+                                              double* M) {
   constexpr int kMine = kList / THREADS;
-  sort_list<THREADS>(s, n);
+  // (neighbours of the wanted bins are sorted to the end)
+  uint32_t mine = 0;
+  for (int i = (int)threadIdx.x; i < n_list; i += THREADS) {
+    if (want.has_x(x_of(value_of(~(uint32_t)(s.list[i] >> 32)), c)))
+      ++mine;
+    else
+      s.list[i] = ~0ull;
+  }
+  const int n = (int)reduce<THREADS>(mine, s.wave_u, Add());
+  sort_list<THREADS>(s, n_list);
   // sums of a bin's integers and tokens up to each token, which start anew with every bin
   u64 q[kMine];
   uint32_t run[kMine];
@@ -715,7 +734,6 @@ __device__ __noinline__ Place resolve_long(Lds& s, Scale c, Cuts x, int n, uint3
 // A band of logits that holds a run of bins, widened by more than its roundings.
 struct Band {
   float end, top;
-  __device__ __forceinline__ bool has(float z) const { return z >= end && z <= top; }
 };
 __device__ __forceinline__ Band band_of(int lo, int hi, const Scale& c) {
   if (hi < lo) return Band{INFINITY, -INFINITY};
@@ -724,11 +742,11 @@ __device__ __forceinline__ Band band_of(int lo, int hi, const Scale& c) {
   return Band{(float)(end - fabs(end) * 0x1p-22 - slack),
               (float)(top + fabs(top) * 0x1p-22 + slack)};
 }
-// Puts the row's tokens of the wanted bins on the list.  Most groups of neighbours have
-// no logit as large as the lowest band's end.
+// Puts the row's tokens of the bands on the list: those of the wanted bins and, now and
+// then, a neighbour.  Most groups of 16 bytes have no logit as large as the lowest band's
+// end.  (n_list counts what does not fit, too.)
 template <int THREADS, int BANDS, bool F32>
-__device__ __forceinline__ void gather(const Row<F32>& r, Lds& s, const Scale& c,
-                                       const Wanted& want, const Band* band) {
+__device__ __forceinline__ void gather(const Row<F32>& r, Lds& s, const Band (&band)[4]) {
   constexpr int E = Row<F32>::kE, U = 8;
   float least = band[0].end;
 #pragma unroll
@@ -749,25 +767,29 @@ __device__ __forceinline__ void gather(const Row<F32>& r, Lds& s, const Scale& c
 #pragma unroll
       for (int e = 1; e < E; ++e) m = fmaxf(m, z[e]);
       if (m >= least && v < r.n_vec) {
+        bool in[E], any = false;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          bool in = band[0].has(z[e]);
+          in[e] = false;
 #pragma unroll
-          for (int k = 1; k < BANDS; ++k) in = in || band[k].has(z[e]);
-          if (in && z[e] > -INFINITY) {
-            const double X = x_of(z[e], c);
-            if (X < kFar && want.has((int)X)) {
+          for (int k = 0; k < BANDS; ++k) in[e] |= (z[e] >= band[k].end) & (z[e] <= band[k].top);
+          any |= in[e];
+        }
+        if (any) {
+#pragma unroll
+          for (int e = 0; e < E; ++e)
+            if (in[e]) {
               const uint32_t to = atomicAdd(&s.n_list, 1u);
-              if (to < (uint32_t)kList) s.list[to] = (u64)(~key_of(z[e])) << 32 | (uint32_t)(v * E + e);
+              if (to < (uint32_t)kList)
+                s.list[to] = (u64)(~key_of(z[e])) << 32 | (uint32_t)(v * E + e);
             }
-          }
         }
       }
     }
   }
 }
 
-// From the filled bins to the token.
+// From the filled bins to the token, which thread 0 gets.
 template <int THREADS, bool F32>
 __device__ __noinline__ Drawn pick(Row<F32> r, Lds& s, Scale c, Settings g, Counts all) {
   constexpr int kPer = kBins / THREADS;
@@ -783,8 +805,35 @@ __device__ __noinline__ Drawn pick(Row<F32> r, Lds& s, Scale c, Settings g, Coun
       n[i] = ns += k;
       step *= 0.9892280131939755;        // 2^(-1 / 64)
     }
-    const double d0 = before_me<THREADS>(ds, s.wave_d);
-    const uint32_t n0 = before_me<THREADS>(ns, s.wave_u);
+    double d0 = ds;
+    uint32_t n0 = ns;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const double o_d = __shfl_up(d0, off);
+      const uint32_t o_n = __shfl_up(n0, off);
+      if ((int)(threadIdx.x % 64) >= off) {
+        d0 += o_d;
+        n0 += o_n;
+      }
+    }
+    if (threadIdx.x % 64 == 63) {
+      s.wave_d[threadIdx.x / 64] = d0;
+      s.wave_u[threadIdx.x / 64] = n0;
+    }
+    __syncthreads();
+    // (what lies before this thread: its wave's part without its own, and the waves')
+    const double up_d = __shfl_up(d0, 1);
+    const uint32_t up_n = __shfl_up(n0, 1);
+    d0 = threadIdx.x % 64 ? up_d : 0.0;
+    n0 = threadIdx.x % 64 ? up_n : 0u;
+    double w_d = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w)
+      if (w < (int)(threadIdx.x / 64)) {
+        w_d += s.wave_d[w];
+        n0 += s.wave_u[w];
+      }
+    d0 += w_d;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       s.cum[threadIdx.x * kPer + i] = d0 + d[i];
@@ -847,21 +896,29 @@ __device__ __noinline__ Drawn pick(Row<F32> r, Lds& s, Scale c, Settings g, Coun
   double M = total;
   Place at;
   if (__builtin_expect(n_want <= (uint32_t)kList, 1)) {
-    Band band[4];
+    Band bands[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) band[i] = band_of(want.lo[3 - i], want.hi[3 - i], c);
-    if (cut_k || cut_p || cut_m)
-      gather<THREADS, 4>(r, s, c, want, band);
+    for (int i = 0; i < 4; ++i) bands[i] = band_of(want.lo[3 - i], want.hi[3 - i], c);
+    // (the draw's is first; of the cuts' often one is left)
+    const int more = (int)cut_k + (int)cut_p + (int)cut_m;
+    if (more == 1) bands[1] = cut_m ? bands[1] : cut_p ? bands[2] : bands[3];
+    if (more == 0)
+      gather<THREADS, 1>(r, s, bands);
+    else if (more == 1)
+      gather<THREADS, 2>(r, s, bands);
     else
-      gather<THREADS, 1>(r, s, c, want, band);
+      gather<THREADS, 4>(r, s, bands);
     __syncthreads();
-    const int n = s.n_list < (uint32_t)kList ? (int)s.n_list : kList;
-    if (n <= 64)
-      at = resolve_short(s, c, cuts, n, &kept, &M);
-    else
-      at = resolve_long<THREADS>(s, c, cuts, n, &kept, &M);
-  } else {
+  }
+  const uint32_t n_list = s.n_list;
+  if (__builtin_expect(n_want > (uint32_t)kList || n_list > (uint32_t)kList, 0)) {
+    __syncthreads();
     at = one_by_one<THREADS>(r, s, c, cuts, &kept, &M);
+  } else if (n_list <= 64) {
+    if (threadIdx.x >= 64) return no_token();       // (the first wave has the result)
+    at = resolve_short(s, c, cuts, want, (int)n_list, &kept, &M);
+  } else {
+    at = resolve_long<THREADS>(s, c, cuts, want, (int)n_list, &kept, &M);
   }
   if (all.min < kept) kept = all.min;        // (tokens past the bins that min_p drops)
   const double lw = -x_of(value_of(at.key), c) * (0.69314718055994530942 / 64.0);
@@ -979,7 +1036,9 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(PieceArgs p) {
   const float m = g.legal ? row_max(p, t) : NAN;
   if (!(fabsf(m) < INFINITY)) return put(p.a, t, no_token());
   const RowBins& from = p.rows[t];
-  for (int b = (int)threadIdx.x; b < kBins; b += kPickThreads) {
+#pragma unroll
+  for (int i = 0; i < kBins / kPickThreads; ++i) {
+    const int b = (int)threadIdx.x + i * kPickThreads;
     s.mass[b] = from.mass[b];
     s.num[b] = from.num[b];
   }
