@@ -210,8 +210,9 @@ __device__ __forceinline__ void clip_chunk(const void* g, void* out, int64_t at,
           for (int e = 0; e < E; e += 4)
             dst[e / 4] = f32x4{x[e] * scale, x[e + 1] * scale, x[e + 2] * scale, x[e + 3] * scale};
         } else if constexpr (GF32) {
-          *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + i) =
-              u32x2{pack_bf16x2(x[0] * scale, x[1] * scale), pack_bf16x2(x[2] * scale, x[3] * scale)};
+          const uint32_t lo = pack_bf16x2(x[0] * scale, x[1] * scale);
+          const uint32_t hi = pack_bf16x2(x[2] * scale, x[3] * scale);
+          *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(out) + i) = u32x2{lo, hi};
         } else {
           u32x4 y;
 #pragma unroll

@@ -23,7 +23,17 @@
 // of a bin are binned again, up to three times, until one logit is left, whose tokens
 // then go by their index.
 //
-// @@BOUND@@
+// Bound.  A row is read twice or three times (maximum, bins, gathered list), the later
+// times out of the caches, and what each logit costs in between (an fp64 product, the
+// polynomial, two LDS atomics: some 40 issue slots a wave and logit) is far more than
+// its two bytes.  512 x 152064 bf16 takes 150 us, of them 25 the maximum, 40 the bins,
+// 7 their scan, 25 the gathering and up to 15 the resolving; read once at the rate of a
+// copy it would take 30.  A work-group of 512 threads holds 49 KB of bins, so two
+// share a CU and one's barriers hide behind the other's logits; four of 256 threads do
+// not fit, one of 1024 took 184 us.  Few rows leave CUs idle, so they are cut into
+// pieces: 8 x 152064 takes 39 us (6 + 9 + 24: maximum, bins, pick) against 57 with a
+// work-group per row; the pick's own gathering (9 us) and its loading and scanning of
+// the bins (8) are latency.
 #include <math.h>
 
 #include "common.hpp"
@@ -37,6 +47,7 @@ namespace {
 typedef unsigned long long u64;
 
 constexpr int kBins = 4096;
+constexpr int kSpare = 64;                 // bins for what lies past them, one per lane
 constexpr double kFar = (double)kBins;     // X of tokens that only count
 constexpr int kList = 2048;                // tokens that are gathered and sorted
 constexpr int kSubs = 1024;                // bins of a refinement
@@ -144,10 +155,10 @@ __device__ __forceinline__ double step_of(int b, const Scale& c) {
 // arithmetic.
 struct Lds {
   union {
-    u64 mass[kBins];         // while the bins fill
+    u64 mass[kBins + kSpare];   // while the bins fill
     double cum[kBins];       // then: cumulative masses
   };
-  uint32_t num[kBins];       // numbers of tokens, then cumulative
+  uint32_t num[kBins + kSpare];  // numbers of tokens, then cumulative
   double group_cum[64];      // of every 64th bin
   uint32_t group_num[64];
   union {
@@ -459,55 +470,109 @@ __device__ __forceinline__ Row<F32> row_of(const SampleArgs& a, int64_t t) {
   return r;
 }
 
-// The largest of a thread's logits; NaN where one of them is NaN.
+// The largest of a thread's logits (NaN where one of them is NaN), and how many of them
+// are masked.
+struct Top {
+  float m;
+  uint32_t masked;
+};
 template <int THREADS, bool F32>
-__device__ __forceinline__ float max_part(const Row<F32>& r, int v0, int v1) {
-  float m = -INFINITY;
+__device__ __forceinline__ Top top_part(const Row<F32>& r, int v0, int v1) {
+  constexpr int E = Row<F32>::kE, U = 8;
+  Top t{-INFINITY, 0};
   bool bad = false;
-  for_each<THREADS, 8>(r, v0, v1, [&](float z, int) {
-    m = fmaxf(m, z);
-    bad = bad || z != z;
-  });
-  return bad ? NAN : m;
+  for (int at = v0 + (int)threadIdx.x; at < v1; at += U * THREADS) {
+    u32x4 q[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int v = at + i * THREADS;
+      q[i] = r.p[v < v1 ? v : at];
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int v = at + i * THREADS;
+      float z[E];
+      logits_of<F32>(q[i], v < v1 ? v : at, r.V, z);
+      float lo = z[0];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        t.m = fmaxf(t.m, z[e]);
+        lo = fminf(lo, z[e]);
+        bad = bad || z[e] != z[e];
+      }
+      if (lo == -INFINITY && v < v1) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) t.masked += z[e] == -INFINITY && v * E + e < r.V;
+      }
+    }
+  }
+  if (bad) t.m = NAN;
+  return t;
 }
 __device__ __forceinline__ float max_or_nan(float a, float b) {
   return a != a ? a : b != b ? b : fmaxf(a, b);
 }
 
-// Tokens that only count, and those that pass min_p (without it: kAll).
+// Tokens that are not masked, and those that pass min_p (without it: kAll).
 constexpr uint32_t kAll = 0xFFFFFFFFu;
 struct Counts {
-  uint32_t far, min;
+  uint32_t live, min;
 };
-// Fills the bins with the logits of vectors [v0, v1); a thread's own Counts.
+// Fills the bins with the logits of vectors [v0, v1); the number of a thread's own that
+// pass min_p.  Without branches (tokens past the bins go to a spare one of the lane), so
+// that the arithmetic of a vector's logits overlaps.
 template <int THREADS, bool MIN, bool F32>
-__device__ __forceinline__ Counts bin_part(const Row<F32>& r, int v0, int v1, Lds& s,
-                                           const Scale& c, double x_min) {
-  Counts n{0, 0};
-  for_each<THREADS, 4>(r, v0, v1, [&](float z, int) {
-    const double X = x_of(z, c);
-    if constexpr (MIN) n.min += X <= x_min;
-    if (X < kFar) {
-      const int b = (int)X;
-      atomicAdd(&s.mass[b], weight_of(X, c));
-      atomicAdd(&s.num[b], 1u);
-    } else if (z > -INFINITY) {
-      ++n.far;
+__device__ __forceinline__ uint32_t bin_part(const Row<F32>& r, int v0, int v1, Lds& s,
+                                             const Scale& c, double x_min) {
+  constexpr int E = Row<F32>::kE, U = 4;
+  const int spare = kBins + (int)(threadIdx.x & 63);
+  uint32_t n_min = 0;
+  for (int at = v0 + (int)threadIdx.x; at < v1; at += U * THREADS) {
+    u32x4 q[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int v = at + i * THREADS;
+      q[i] = r.p[v < v1 ? v : at];
     }
-  });
-  return n;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      const int v = at + i * THREADS;
+      if (v >= v1) break;
+      float z[E];
+      logits_of<F32>(q[i], v, r.V, z);
+      double X[E];
+      u64 w[E];
+      int b[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) X[e] = x_of(z[e], c);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        b[e] = (int)X[e];
+        b[e] = (uint32_t)b[e] < (uint32_t)kBins ? b[e] : spare;
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) w[e] = weight_of(X[e], c);
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if constexpr (MIN) n_min += X[e] <= x_min;
+        atomicAdd(&s.mass[b[e]], w[e]);
+        atomicAdd(&s.num[b[e]], 1u);
+      }
+    }
+  }
+  return n_min;
 }
+// (the sum over the work-group)
 template <int THREADS, bool F32>
-__device__ __forceinline__ Counts fill_bins(const Row<F32>& r, int v0, int v1, Lds& s,
-                                            const Scale& c, float min_p) {
-  Counts n;
-  if (min_p > 0.0f)
-    n = bin_part<THREADS, true>(r, v0, v1, s, c, -64.0 * log2((double)min_p));
-  else
-    n = bin_part<THREADS, false>(r, v0, v1, s, c, 0.0);
-  n.far = reduce<THREADS>(n.far, s.wave_u, Add());
-  n.min = min_p > 0.0f ? reduce<THREADS>(n.min, s.wave_u, Add()) : kAll;
-  return n;
+__device__ __forceinline__ uint32_t fill_bins(const Row<F32>& r, int v0, int v1, Lds& s,
+                                              const Scale& c, float min_p) {
+  if (!(min_p > 0.0f)) {
+    bin_part<THREADS, false>(r, v0, v1, s, c, 0.0);
+    __syncthreads();
+    return kAll;
+  }
+  return reduce<THREADS>(bin_part<THREADS, true>(r, v0, v1, s, c, -64.0 * log2((double)min_p)),
+                         s.wave_u, Add());
 }
 
 // Bins that hold what the targets need: single ones and runs.
@@ -847,7 +912,7 @@ __device__ __noinline__ Drawn pick(Row<F32> r, Lds& s, Scale c, Settings g, Coun
     __syncthreads();
   }
   const double total = s.cum[kBins - 1];
-  const uint32_t near = s.num[kBins - 1], live = near + all.far;
+  const uint32_t near = s.num[kBins - 1], live = all.live;
   auto mass_before = [&](int b) { return b > 0 ? s.cum[b - 1] : 0.0; };
   auto num_before = [&](int b) { return b > 0 ? s.num[b - 1] : 0u; };
 
@@ -926,7 +991,7 @@ __device__ __noinline__ Drawn pick(Row<F32> r, Lds& s, Scale c, Settings g, Coun
 }
 
 __device__ __forceinline__ void clear_bins(Lds& s, int threads) {
-  for (int i = (int)threadIdx.x; i < kBins; i += threads) {
+  for (int i = (int)threadIdx.x; i < kBins + kSpare; i += threads) {
     s.mass[i] = 0;
     s.num[i] = 0;
   }
@@ -945,11 +1010,13 @@ __global__ __launch_bounds__(kRowThreads, 4) void sample_rows_kernel(SampleArgs 
   if (!g.legal) return put(a, t, no_token());
   const Row<F32> r = row_of<F32>(a, t);
   clear_bins(s, kRowThreads);
-  const float m = reduce<kRowThreads>(max_part<kRowThreads>(r, 0, r.n_vec),
-                                      reinterpret_cast<float*>(s.wave_u), max_or_nan);
+  const Top top = top_part<kRowThreads>(r, 0, r.n_vec);
+  const float m = reduce<kRowThreads>(top.m, reinterpret_cast<float*>(s.wave_u), max_or_nan);
   if (!(fabsf(m) < INFINITY)) return put(a, t, no_token());
+  Counts n;
+  n.live = (uint32_t)r.V - reduce<kRowThreads>(top.masked, s.wave_u, Add());
   const Scale c = scale_of(m, g.tau, unit);
-  const Counts n = fill_bins<kRowThreads>(r, 0, r.n_vec, s, c, g.min_p);
+  n.min = fill_bins<kRowThreads>(r, 0, r.n_vec, s, c, g.min_p);
   put(a, t, pick<kRowThreads>(r, s, c, g, n));
 }
 
@@ -960,24 +1027,28 @@ constexpr int kPieceThreads = 512, kPickThreads = 1024;
 struct RowBins {
   u64 mass[kBins];
   uint32_t num[kBins];
-  uint32_t far, min;
-  uint32_t pad[62];
+  uint32_t min;
+  uint32_t pad[63];
 };
 struct PieceArgs {
   SampleArgs a;
   double unit;
   int pieces, vecs;     // of a row; 16-byte vectors of a piece
   RowBins* rows;
-  float* max;           // [row][piece]
+  Top* top;             // [row][piece]
 };
 
-__device__ __forceinline__ float row_max(const PieceArgs& p, int64_t t) {
-  // (at most 64 pieces: one a lane)
+// (at most 64 pieces: one a lane)
+__device__ __forceinline__ Top row_top(const PieceArgs& p, int64_t t) {
   const int lane = threadIdx.x & 63;
-  float m = p.max[t * p.pieces + (lane < p.pieces ? lane : 0)];
+  Top x = p.top[t * p.pieces + (lane < p.pieces ? lane : 0)];
+  if (lane >= p.pieces) x.masked = 0;
 #pragma unroll
-  for (int off = 32; off > 0; off >>= 1) m = max_or_nan(m, __shfl_xor(m, off));
-  return m;
+  for (int off = 32; off > 0; off >>= 1) {
+    x.m = max_or_nan(x.m, __shfl_xor(x.m, off));
+    x.masked += __shfl_xor(x.masked, off);
+  }
+  return x;
 }
 
 template <bool F32>
@@ -995,9 +1066,10 @@ __global__ __launch_bounds__(kPieceThreads) void piece_max_kernel(PieceArgs p) {
   if (g.left_out || !g.legal) return;
   const Row<F32> r = row_of<F32>(p.a, t);
   const int64_t v0 = (int64_t)i * p.vecs, v1 = v0 + p.vecs < r.n_vec ? v0 + p.vecs : r.n_vec;
-  const float m = reduce<kPieceThreads>(max_part<kPieceThreads>(r, (int)v0, (int)v1), lds,
-                                        max_or_nan);
-  if (threadIdx.x == 0) p.max[blockIdx.x] = m;
+  Top top = top_part<kPieceThreads>(r, (int)v0, (int)v1);
+  top.m = reduce<kPieceThreads>(top.m, lds, max_or_nan);
+  top.masked = reduce<kPieceThreads>(top.masked, reinterpret_cast<uint32_t*>(lds), Add());
+  if (threadIdx.x == 0) p.top[blockIdx.x] = top;
 }
 
 template <bool F32>
@@ -1007,24 +1079,21 @@ __global__ __launch_bounds__(kPieceThreads) void piece_bins_kernel(PieceArgs p) 
   const int i = blockIdx.x % p.pieces;
   const Settings g = settings_of(p.a, t);
   if (g.left_out || !g.legal) return;
-  const float m = row_max(p, t);
+  const float m = row_top(p, t).m;
   if (!(fabsf(m) < INFINITY)) return;
   clear_bins(s, kPieceThreads);
   __syncthreads();
   const Row<F32> r = row_of<F32>(p.a, t);
   const Scale c = scale_of(m, g.tau, p.unit);
   const int64_t v0 = (int64_t)i * p.vecs, v1 = v0 + p.vecs < r.n_vec ? v0 + p.vecs : r.n_vec;
-  const Counts n = fill_bins<kPieceThreads>(r, (int)v0, (int)v1, s, c, g.min_p);
+  const uint32_t n_min = fill_bins<kPieceThreads>(r, (int)v0, (int)v1, s, c, g.min_p);
   RowBins& to = p.rows[t];
   for (int b = (int)threadIdx.x; b < kBins; b += kPieceThreads)
     if (s.num[b] != 0) {
       atomicAdd(&to.mass[b], s.mass[b]);
       atomicAdd(&to.num[b], s.num[b]);
     }
-  if (threadIdx.x == 0) {
-    if (n.far) atomicAdd(&to.far, n.far);
-    if (n.min != kAll && n.min) atomicAdd(&to.min, n.min);
-  }
+  if (threadIdx.x == 0 && n_min != kAll && n_min != 0) atomicAdd(&to.min, n_min);
 }
 
 template <bool F32>
@@ -1033,8 +1102,9 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(PieceArgs p) {
   const int64_t t = blockIdx.x;
   const Settings g = settings_of(p.a, t);
   if (g.left_out) return put(p.a, t, left_out());
-  const float m = g.legal ? row_max(p, t) : NAN;
-  if (!(fabsf(m) < INFINITY)) return put(p.a, t, no_token());
+  if (!g.legal) return put(p.a, t, no_token());
+  const Top top = row_top(p, t);
+  if (!(fabsf(top.m) < INFINITY)) return put(p.a, t, no_token());
   const RowBins& from = p.rows[t];
 #pragma unroll
   for (int i = 0; i < kBins / kPickThreads; ++i) {
@@ -1042,13 +1112,14 @@ __global__ __launch_bounds__(kPickThreads) void pick_kernel(PieceArgs p) {
     s.mass[b] = from.mass[b];
     s.num[b] = from.num[b];
   }
-  const Counts n{from.far, g.min_p > 0.0f ? from.min : kAll};
+  const Counts n{(uint32_t)p.a.vocab - top.masked, g.min_p > 0.0f ? from.min : kAll};
   __syncthreads();
-  put(p.a, t, pick<kPickThreads>(row_of<F32>(p.a, t), s, scale_of(m, g.tau, p.unit), g, n));
+  put(p.a, t, pick<kPickThreads>(row_of<F32>(p.a, t), s, scale_of(top.m, g.tau, p.unit), g, n));
 }
 
-// Pieces of a row: about two work-groups a CU in all, of at least 1024 vectors (a
-// piece's bins cost it about as much as these); one: a work-group per row.
+// Pieces of a row: about a work-group a CU in all (256), each of at least 512 vectors
+// (clearing and adding up its bins costs a piece about as much), and at most 64; one: a
+// work-group per row.
 int pieces_of(int64_t n_tok, int64_t vocab) {
   const int64_t vecs = vocab / 8;
   int64_t most = vecs / 512, want = 256 / (n_tok > 0 ? n_tok : 1);
@@ -1062,7 +1133,8 @@ int pieces_of(int64_t n_tok, int64_t vocab) {
 size_t sample_ws_bytes(int64_t n_tok, int64_t vocab) {
   const int pieces = pieces_of(n_tok, vocab);
   if (n_tok == 0 || pieces == 1) return 0;
-  return (size_t)n_tok * sizeof(RowBins) + (size_t)round_up(n_tok * pieces * 4, 256);
+  return (size_t)n_tok * sizeof(RowBins) +
+         (size_t)round_up(n_tok * pieces * (int64_t)sizeof(Top), 256);
 }
 
 hipError_t launch_sample(const SampleArgs& a, bool f32, char* ws, hipStream_t s) {
@@ -1083,7 +1155,7 @@ hipError_t launch_sample(const SampleArgs& a, bool f32, char* ws, hipStream_t s)
   const int64_t n_vec = ((int64_t)a.vocab + e - 1) / e;
   PieceArgs p{a, unit, pieces, (int)((n_vec + pieces - 1) / pieces),
               reinterpret_cast<RowBins*>(ws),
-              reinterpret_cast<float*>(ws + (size_t)a.n_tok * sizeof(RowBins))};
+              reinterpret_cast<Top*>(ws + (size_t)a.n_tok * sizeof(RowBins))};
   const dim3 grid((unsigned)(a.n_tok * pieces));
   if (f32) {
     hipLaunchKernelGGL(piece_max_kernel<true>, grid, dim3(kPieceThreads), 0, s, p);
