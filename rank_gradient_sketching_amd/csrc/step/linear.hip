@@ -113,9 +113,17 @@ __device__ __forceinline__ void load_bias(const GemmArgs& g, int n, float* b) {
                         : bf16_to_f32(static_cast<const uint16_t*>(g.bias)[n + e]);
   }
 }
-// Columns n .. n + 7 of row m (n a multiple of 8, below N), from the sums v.
+// The residual there (zeros without one, and outside the result).
+__device__ __forceinline__ u32x4 load_residual(const GemmArgs& g, int m, int n) {
+  u32x4 q{0, 0, 0, 0};
+  if (g.add != nullptr && m < g.M && n < g.N)
+    q = *reinterpret_cast<const u32x4*>(g.add + (int64_t)m * g.ldadd + n);
+  return q;
+}
+// Columns n .. n + 7 of row m (n a multiple of 8, below N), from the sums v and the
+// residual q.
 __device__ __forceinline__ void epilogue8(const GemmArgs& g, int m, int n, const float* bias,
-                                          float* v) {
+                                          u32x4 q, float* v) {
   const int valid = g.N - n;
 #pragma unroll
   for (int e = 0; e < 8; ++e) v[e] += bias[e];
@@ -132,7 +140,6 @@ __device__ __forceinline__ void epilogue8(const GemmArgs& g, int m, int n, const
     for (int e = 0; e < 8; ++e) v[e] = activate_any(v[e], g.act);
   }
   if (g.add != nullptr) {
-    const u32x4 q = *reinterpret_cast<const u32x4*>(g.add + (int64_t)m * g.ldadd + n);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       v[2 * e] += bf16_lo(q[e]);
@@ -283,16 +290,26 @@ __device__ __forceinline__ Place place_of(const GemmArgs& g, const TileGrid& t) 
 // Ends a tile: the wave's MI x NI blocks of 16 x 16 (rows m0 .., columns n0 ..) pass
 // through its own part of LDS, 32 rows at a time, so that the epilogue is one loop over
 // whole rows and not code for every register.  LDS rows lie four words apart in the
-// banks.  All waves have done with the operands.
+// banks.  All waves have done with the operands.  The residual of a pass is loaded during
+// the one before: read where it was added, behind the stores of the rows before it, it
+// cost 8192 x 4096 x 4096 with gelu, residual and pre 272 us instead of 257.
 template <int MI, int NI>
 __device__ __forceinline__ void finish(const GemmArgs& g, const TileGrid& t, int split, int m0,
                                        int n0, const f32x4 (&acc)[MI][NI], float* mine, int lane) {
   constexpr int kCols = NI * 16, kPitch = kCols + 4, kPass = 32;
   constexpr int kLanes = kCols / 8;      // of a row
-  static_assert(MI % 2 == 0, "whole passes");
+  constexpr int kRows = 64 / kLanes;     // rows at once
+  constexpr int kGroups = kPass / kRows;
+  static_assert(MI % 2 == 0 && kPass % kRows == 0, "whole passes");
   const int n = n0 + 8 * (lane % kLanes);
   float bias[8];
   load_bias(g, n, bias);
+  const bool whole = t.splits == 1;
+  // the residual of a pass is on its way during the pass before it
+  u32x4 q[kGroups];
+#pragma unroll
+  for (int i = 0; i < kGroups; ++i)
+    q[i] = load_residual(g, whole ? m0 + lane / kLanes + i * kRows : g.M, n);
   for (int pass = 0; pass < MI / 2; ++pass) {
 #pragma unroll
     for (int i = 0; i < MI; ++i) {
@@ -303,17 +320,19 @@ __device__ __forceinline__ void finish(const GemmArgs& g, const TileGrid& t, int
                                     4 * (lane >> 4)) = acc[i][j];
       }
     }
-#pragma unroll 2
-    for (int r = lane / kLanes; r < kPass; r += 64 / kLanes) {
-      const int m = m0 + pass * kPass + r;
+#pragma unroll
+    for (int i = 0; i < kGroups; ++i) {
+      const int r = lane / kLanes + i * kRows, m = m0 + pass * kPass + r;
+      const u32x4 add = q[i];
+      q[i] = load_residual(g, whole && pass + 1 < MI / 2 ? m + kPass : g.M, n);
       float v[8];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
         *reinterpret_cast<f32x4*>(v + 4 * h) =
             *reinterpret_cast<const f32x4*>(mine + r * kPitch + 8 * (lane % kLanes) + 4 * h);
       if (m >= g.M || n >= g.N) continue;
-      if (t.splits == 1) {
-        epilogue8(g, m, n, bias, v);
+      if (whole) {
+        epilogue8(g, m, n, bias, add, v);
       } else {
         f32x4* const p =
             reinterpret_cast<f32x4*>(t.partial + ((int64_t)split * g.M + m) * t.n8 + n);
@@ -527,6 +546,7 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs g, TileGrid t) {
        i += (int64_t)gridDim.x * 256) {
     const int m = (int)(i / groups), n = (int)(i % groups) * 8;
     const float* p = t.partial + (int64_t)m * t.n8 + n;
+    const u32x4 add = load_residual(g, m, n);
     f32x4 lo = *reinterpret_cast<const f32x4*>(p), hi = *reinterpret_cast<const f32x4*>(p + 4);
     for (int s = 1; s < t.splits; ++s) {
       p += (int64_t)g.M * t.n8;
@@ -540,7 +560,7 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs g, TileGrid t) {
       v[e] = lo[e];
       v[4 + e] = hi[e];
     }
-    epilogue8(g, m, n, bias, v);
+    epilogue8(g, m, n, bias, add, v);
   }
 }
 
@@ -565,6 +585,15 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(GemmArgs g) {
   const int blocks = g.K / 64, per = (blocks + kFewWaves - 1) / kFewWaves;
   const int b0 = wave * per < blocks ? wave * per : blocks;
   const int b1 = b0 + per < blocks ? b0 + per : blocks;
+  // bias and residual of the eight results that this thread will end
+  const int m = (int)threadIdx.x >> 1, n = n0 + 8 * ((int)threadIdx.x & 1);
+  const bool ends = m < 16 && m < g.M && n < g.N;
+  float bias[8];
+  u32x4 add{0, 0, 0, 0};
+  if (ends) {
+    load_bias(g, n, bias);
+    add = load_residual(g, m, n);
+  }
   constexpr int kDeep = 4;     // blocks in flight
   for (int b = b0; b < b1; b += kDeep) {
     u32x4 wv[2 * kDeep], xv[2 * kDeep];
@@ -591,10 +620,8 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(GemmArgs g) {
   // (a lane holds row i of C, columns 4 q .. 4 q + 3)
   *reinterpret_cast<f32x4*>(&sums[wave][i][4 * q]) = acc;
   __syncthreads();
-  const int m = (int)threadIdx.x >> 1, n = n0 + 8 * ((int)threadIdx.x & 1);
-  if (m >= 16 || m >= g.M || n >= g.N) return;
-  float v[8], bias[8];
-  load_bias(g, n, bias);
+  if (!ends) return;
+  float v[8];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     f32x4 s{0, 0, 0, 0};
@@ -604,7 +631,7 @@ __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(GemmArgs g) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[4 * h + e] = s[e];
   }
-  epilogue8(g, m, n, bias, v);
+  epilogue8(g, m, n, bias, add, v);
 }
 
 // ------------------------------------------------------------------ which kernel
@@ -702,32 +729,37 @@ void launch_tiles(const GemmArgs& a, const TilePlan& p, hipStream_t s) {
 }
 
 // ------------------------------------------------------------------ activation gradient
-constexpr int kColThreads = 32, kRowLanes = 8;     // a work-group: 256 columns
-constexpr int kStripCols = kColThreads * 8;
+// A work-group takes 8 COLS columns, its THREADS / COLS row lanes each every so manieth
+// row: 256 columns and 8 lanes, or, for few rows (which one work-group then adds up alone,
+// without a second launch), 16 columns and 256 lanes.
+constexpr int kStripCols = 256, kRowLanes = 8, kNarrowCols = 16, kNarrowThreads = 512;
 
 struct ActGrid {
+  bool narrow;
   int rows;              // of a work-group
   int chunks;            // work-groups along T
   float* partial;        // [chunks][d], or d_bias itself
 };
 
-// Each thread takes eight columns of every eighth row, four rows' loads in flight.
-template <int ACT, bool F32>
-__global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a, ActGrid t) {
-  constexpr int U = 4;
-  __shared__ float sums[kRowLanes][kStripCols];
-  const int cl = (int)threadIdx.x % kColThreads, rl = (int)threadIdx.x / kColThreads;
-  const int n = ((int)blockIdx.x * kColThreads + cl) * 8;
+// Each thread takes eight columns of its rows, four rows' loads in flight.
+template <int ACT, bool F32, int COLS, int THREADS>
+__global__ __launch_bounds__(THREADS) void act_grad_kernel(ActGradArgs a, ActGrid t) {
+  constexpr int U = 4, kLanes = THREADS / COLS, kWaves = THREADS / 64;
+  __shared__ float sums[kWaves][COLS * 8];
+  const int cl = (int)threadIdx.x % COLS, rl = (int)threadIdx.x / COLS;
+  // (narrow strips that share lines of 128 bytes go to one L2)
+  const int strip = COLS < 8 ? xcd_runs((int)blockIdx.x, (int)gridDim.x) : (int)blockIdx.x;
+  const int n = (strip * COLS + cl) * 8;
   const int64_t r0 = (int64_t)blockIdx.y * t.rows;
   const int64_t r1 = r0 + t.rows < a.T ? r0 + t.rows : a.T;
   const int valid = a.d - n;
   float sum[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (valid > 0) {
-    for (int64_t r = r0 + rl; r < r1; r += U * kRowLanes) {
+    for (int64_t r = r0 + rl; r < r1; r += U * kLanes) {
       u32x4 lo[U], hi[U], pre[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t row = r + u * kRowLanes < r1 ? r + u * kRowLanes : r;
+        const int64_t row = r + u * kLanes < r1 ? r + u * kLanes : r;
         if constexpr (F32) {
           // (a row's padding ends on 16 bytes of fp32, not of eight entries)
           const u32x4* const p = reinterpret_cast<const u32x4*>(
@@ -743,7 +775,7 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a, ActGrid t)
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t row = r + u * kRowLanes;
+        const int64_t row = r + u * kLanes;
         if (row >= r1) break;
         float g[8];
 #pragma unroll
@@ -777,14 +809,21 @@ __global__ __launch_bounds__(256) void act_grad_kernel(ActGradArgs a, ActGrid t)
     }
   }
   if (a.d_bias == nullptr) return;
+  // the wave's row lanes, then the waves
 #pragma unroll
-  for (int e = 0; e < 8; ++e) sums[rl][cl * 8 + e] = sum[e];
+  for (int off = COLS; off < 64; off *= 2)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] += __shfl_xor(sum[e], off);
+  if ((threadIdx.x & 63) < COLS) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sums[threadIdx.x >> 6][cl * 8 + e] = sum[e];
+  }
   __syncthreads();
-  const int c = (int)blockIdx.x * kStripCols + (int)threadIdx.x;
-  if (c >= a.d) return;
+  const int c = strip * COLS * 8 + (int)threadIdx.x;
+  if (threadIdx.x >= COLS * 8 || c >= a.d) return;
   float v = 0;
 #pragma unroll
-  for (int i = 0; i < kRowLanes; ++i) v += sums[i][threadIdx.x];
+  for (int i = 0; i < kWaves; ++i) v += sums[i][threadIdx.x];
   t.partial[(int64_t)blockIdx.y * a.d + c] = v;
 }
 
@@ -807,8 +846,18 @@ __global__ __launch_bounds__(256) void bias_join_kernel(const float* __restrict_
              (sums[2][threadIdx.x] + sums[3][threadIdx.x]);
 }
 
-ActGrid make_act_grid(int64_t T, int64_t d) {
+// Narrow up to 1024 rows and 640 work-groups.  With
+// silu, narrow against strips and their join: 16 x 4096 3.1 us, 4.7; 501 x 1001 4.2, 6.8;
+// 1024 x 4096 7.6, 8.4; 1024 x 16384 23.3, 20.5; 2048 x 4096 14.6, 13.1.  (32 columns a
+// work-group: 501 x 1001 5.3, the slopes of too few CUs.)
+ActGrid make_act_grid(int64_t T, int64_t d, bool sums) {
   ActGrid g{};
+  g.narrow = sums && T <= 1024 && d <= 640 * kNarrowCols;
+  if (g.narrow) {
+    g.rows = (int)T;
+    g.chunks = 1;
+    return g;
+  }
   const int64_t strips = (d + kStripCols - 1) / kStripCols;
   int64_t chunks = (1024 + strips - 1) / strips;
   const int64_t most = (T + kRowLanes - 1) / kRowLanes;
@@ -823,11 +872,17 @@ ActGrid make_act_grid(int64_t T, int64_t d) {
 
 template <int ACT>
 void launch_act(const ActGradArgs& a, const ActGrid& g, hipStream_t s) {
-  const dim3 grid((unsigned)((a.d + kStripCols - 1) / kStripCols), (unsigned)g.chunks);
-  if (a.d_out_f32)
-    hipLaunchKernelGGL((act_grad_kernel<ACT, true>), grid, dim3(256), 0, s, a, g);
-  else
-    hipLaunchKernelGGL((act_grad_kernel<ACT, false>), grid, dim3(256), 0, s, a, g);
+  const int cols = g.narrow ? kNarrowCols : kStripCols;
+  const dim3 grid((unsigned)((a.d + cols - 1) / cols), (unsigned)g.chunks);
+  const dim3 block(g.narrow ? kNarrowThreads : 256);
+  constexpr int kN = kNarrowCols / 8, kS = kStripCols / 8;
+  constexpr int kNT = kNarrowThreads;
+  auto kernel = a.d_out_f32 ? act_grad_kernel<ACT, true, kS, 256>
+                            : act_grad_kernel<ACT, false, kS, 256>;
+  if (g.narrow)
+    kernel = a.d_out_f32 ? act_grad_kernel<ACT, true, kN, kNT>
+                         : act_grad_kernel<ACT, false, kN, kNT>;
+  hipLaunchKernelGGL(kernel, grid, block, 0, s, a, g);
 }
 
 }  // namespace
@@ -864,12 +919,12 @@ hipError_t launch_gemm(GemmForm form, const GemmArgs& a, char* ws, hipStream_t s
 }
 
 size_t act_grad_ws_bytes(int64_t T, int64_t d) {
-  const ActGrid g = make_act_grid(T, d);
+  const ActGrid g = make_act_grid(T, d, true);
   return g.chunks > 1 ? (size_t)round_up((int64_t)g.chunks * d * 4, 256) : 0;
 }
 
 hipError_t launch_act_grad(const ActGradArgs& a, char* ws, hipStream_t s) {
-  ActGrid g = make_act_grid(a.T, a.d);
+  ActGrid g = make_act_grid(a.T, a.d, a.d_bias != nullptr);
   if (g.chunks < 1) g.chunks = 1;      // (no rows: the sums are zero)
   g.partial = g.chunks > 1 ? reinterpret_cast<float*>(ws) : a.d_bias;
   switch (a.act) {

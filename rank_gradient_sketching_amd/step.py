@@ -70,9 +70,11 @@ def sample_tokens(z, u, tau=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, ws=Non
             raise ValueError(f"top_k must be between 0 and 2^31 - 1 (got {x})")
         scalars.append(default if per_row else x)
     if out is None:
-        out = SampledTokens(torch.empty(n, dtype=torch.int64, device=z.device),
-                            *torch.empty((2, n), dtype=torch.float32, device=z.device).unbind(0),
-                            torch.empty(n, dtype=torch.int32, device=z.device))
+        device = z.device
+        out = SampledTokens(torch.empty(n, dtype=torch.int64, device=device),
+                            torch.empty(n, dtype=torch.float32, device=device),
+                            torch.empty(n, dtype=torch.float32, device=device),
+                            torch.empty(n, dtype=torch.int32, device=device))
         ptrs = [t.data_ptr() for t in out]
     else:
         _need(out.token, "out.token", _I64, dev, (n,), contiguous=True)
@@ -133,7 +135,7 @@ def grad_norm_bind(grads, out=None):
         dev = g.get_device()
         q, at, k = items[i], g.data_ptr(), g.numel()
         q.g, q.n, q.g_type = at, k, _TYPES[g.dtype]
-        keep.append(g)
+        keep.append(g.untyped_storage())
         in_place = o is None
         if not in_place:
             _need(o, f"out[{i}]", _EITHER, dev, contiguous=True)
@@ -141,13 +143,12 @@ def grad_norm_bind(grads, out=None):
                 raise ValueError(f"out[{i}] must have {k} entries (got {o.numel()})")
             to = o.data_ptr()
             q.out, q.out_type = to, _TYPES[o.dtype]
-            keep.append(o)
+            keep.append(o.untyped_storage())
             in_place = to == at and o.dtype == g.dtype
             if not in_place:
                 spans.append((to, to + k * o.element_size(), True, ("out", i)))
         spans.append((at, at + k * g.element_size(), in_place, ("grads", i)))
     _check_apart(spans)
-    keep = [t.detach() for t in keep]
     size = int(_lib.lib().logra_grad_table_bytes(n))
     if size == 0:
         raise ValueError(f"{n} tensors are too many for one handle")
@@ -177,11 +178,11 @@ def grad_norm(bound, max_norm=None, grad_scale=None, norm_type=2, per_tensor=Fal
         s_ptr = grad_scale.data_ptr()
     like = bound.table_dev
     if out is None:
-        both = torch.empty(2, dtype=torch.float32, device=like.device)
-        norms = None
-        if per_tensor:
-            norms = torch.empty(bound.n, dtype=torch.float32, device=like.device)
-        out = GradNorm(both[:1], both[1:], norms)
+        device = bound.device      # (new tensors cost the host less than views of one)
+        out = GradNorm(torch.empty(1, dtype=torch.float32, device=device),
+                       torch.empty(1, dtype=torch.float32, device=device),
+                       torch.empty(bound.n, dtype=torch.float32, device=device)
+                       if per_tensor else None)
     else:
         for name in ("norm", "scale"):
             _need(getattr(out, name), f"out.{name}", _F32, dev, (1,))
