@@ -185,3 +185,21 @@ def test_sketch_norm_estimates_the_gradients(lg):
         squares.append(lg.grad_norm(lg.grad_norm_bind([S])).norm.item() ** 2)
     # one sketch's square spreads by at most sqrt(2 / r) of it: four deviations of 24
     assert abs(np.mean(squares) / G ** 2 - 1) < 4 * np.sqrt(2 / r / 24)
+
+
+@pytest.mark.parametrize("gt,ot", [(BF, None), (BF, F32), (F32, BF), (F32, None)])
+def test_clip_past_the_caches(lg, gt, ot):
+    """Enough gradients (128 MiB) for the loads and stores that pass the caches, beside a
+    small tensor; products of fp32 rounded once, as torch's own."""
+    n = (72_000_005 if gt == BF else 36_000_003)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    gs = [torch.randn(m, device="cuda", generator=g).to(gt) for m in (n, 13)]
+    want = [(x.float() * 0.375).to(ot or gt) for x in gs]
+    outs = None if ot is None else [torch.full_like(x, float("nan"), dtype=ot) for x in gs]
+    b = lg.grad_norm_bind(gs, out=outs)
+    norm = lg.grad_norm(b).norm.item()
+    ref = np.sqrt(sum(float(x.double().square().sum()) for x in gs))
+    assert abs(norm - ref) <= 1.001 * U * ref
+    lg.grad_clip(b, torch.tensor([0.375], device="cuda"))
+    assert all(torch.equal(x, w) for x, w in zip(gs if ot is None else outs, want))
