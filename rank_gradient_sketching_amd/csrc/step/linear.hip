@@ -15,8 +15,7 @@
 // under them; a loop of nothing but 32x32x16 products of random numbers reaches 1830
 // TFLOP/s, 16x16x32 ones 1700): 8192 x 4096 x 4096 takes 200, 198 and 199 us in the three
 // forms (1380 TFLOP/s; the library's products 175 - 200, 201 and 230); the weights' HBM
-// bytes for few rows (64 x 1536 to 152064 fp32 results: 97 us, 5.2 TB/s).
-//
+// bytes for few rows (64 x 1536 to 152064 fp32 results: 102 us, 5.0 TB/s).
 #include <math.h>
 
 #include "common.hpp"
@@ -208,10 +207,16 @@ struct Operand {
     }
   }
   // Copies [i0, i1) of this lane's next step; a step's copies are issued once each.
+  // ONCE: of an operand that no other work-group reads.
+  template <bool ONCE = false>
   __device__ __forceinline__ void copy(uint32_t lds, int wave, int i0 = 0, int i1 = kDma) {
 #pragma unroll
     for (int i = i0; i < i1; ++i) {
-      lds_dma16(src[i], lds + (uint32_t)(wave * kDma + i) * 1024u);
+      const uint32_t to = lds + (uint32_t)(wave * kDma + i) * 1024u;
+      if constexpr (ONCE)
+        lds_dma16_nt(src[i], to);
+      else
+        lds_dma16(src[i], to);
       src[i] += advance;
     }
   }
@@ -471,8 +476,10 @@ __global__ __launch_bounds__(kBigThreads) void big_kernel(GemmArgs g, TileGrid t
 // the memory's latency is paid once and not in every step.
 // 64 x 64 with four stages and 64 x 128 with three leave room for two work-groups on a
 // CU (64 x 128 with four stages has a CU to itself: 200 x 1536 to 8960 21 us, with
-// three 18; 128 x 128 is no faster than 64 x 128 anywhere).
-template <int BM, int BN, int WM, int WN, int STAGES, bool AK, bool BK>
+// three 18; 128 x 128 is no faster than 64 x 128 anywhere).  ONCE: results of one tile of
+// rows, whose weights no other work-group reads, copied past the caches (64 x 1536 to
+// 152064 109 -> 102 us, 32 x 4096 to 32000 57 -> 51; few_rows_kernel lost by it).
+template <int BM, int BN, int WM, int WN, int STAGES, bool AK, bool BK, bool ONCE>
 __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(GemmArgs g, TileGrid t) {
   constexpr int NW = WM * WN, MI = BM / WM / 16, NI = BN / WN / 16;
   typedef Operand<BM, NW, AK> OpA;
@@ -498,7 +505,7 @@ __global__ __launch_bounds__(WM* WN * 64) void tile_kernel(GemmArgs g, TileGrid 
     const uint32_t to = (uint32_t)(k % STAGES) * kStage;
     if (k < whole) {
       a.copy(base + to, wave);
-      b.copy(base + to + OpA::kBytes, wave);
+      b.template copy<ONCE>(base + to + OpA::kBytes, wave);
     } else if (k < steps) {
       a.copy_last(lds + to, wave, lane, at.left);
       b.copy_last(lds + to + OpA::kBytes, wave, lane, at.left);
@@ -715,10 +722,20 @@ void launch_tiles(const GemmArgs& a, const TilePlan& p, hipStream_t s) {
   const dim3 block((unsigned)kKinds[p.tile].threads);
   switch (p.tile) {
     case kTile64:
-      hipLaunchKernelGGL((tile_kernel<64, 64, 2, 2, 4, AK, BK>), grid, block, 0, s, a, p.grid);
+      if (p.grid.tiles_m == 1)
+        hipLaunchKernelGGL((tile_kernel<64, 64, 2, 2, 4, AK, BK, true>), grid, block, 0, s, a,
+                           p.grid);
+      else
+        hipLaunchKernelGGL((tile_kernel<64, 64, 2, 2, 4, AK, BK, false>), grid, block, 0, s, a,
+                           p.grid);
       break;
     case kTile64x128:
-      hipLaunchKernelGGL((tile_kernel<64, 128, 2, 2, 3, AK, BK>), grid, block, 0, s, a, p.grid);
+      if (p.grid.tiles_m == 1)
+        hipLaunchKernelGGL((tile_kernel<64, 128, 2, 2, 3, AK, BK, true>), grid, block, 0, s, a,
+                           p.grid);
+      else
+        hipLaunchKernelGGL((tile_kernel<64, 128, 2, 2, 3, AK, BK, false>), grid, block, 0, s, a,
+                           p.grid);
       break;
     case kTile256x128:
       hipLaunchKernelGGL((big_kernel<128, AK, BK>), grid, block, 0, s, a, p.grid);
