@@ -74,7 +74,7 @@ __device__ __forceinline__ void logits_of(const u32x4& q, int v, int V, float* z
   }
 }
 
-// f(z, index) for the logits of vectors [v0, v1) of the row, U loads in flight.
+// f(z) for the logits of vectors [v0, v1) of the row, U loads in flight.
 template <int THREADS, int U, bool F32, class F>
 __device__ __forceinline__ void for_each(const Row<F32>& r, int v0, int v1, F f) {
   constexpr int E = Row<F32>::kE;
@@ -92,7 +92,7 @@ __device__ __forceinline__ void for_each(const Row<F32>& r, int v0, int v1, F f)
         float z[E];
         logits_of<F32>(q[i], v, r.V, z);
 #pragma unroll
-        for (int e = 0; e < E; ++e) f(z[e], v * E + e);
+        for (int e = 0; e < E; ++e) f(z[e]);
       }
     }
   }
@@ -296,7 +296,7 @@ __device__ __noinline__ Place refine(Row<F32> r, Lds& s, Scale c, int b, Target 
   const double before = b ? s.cum[b - 1] : 0.0, step = step_of(b, c);
   const uint32_t n_before = b ? s.num[b - 1] : 0u;
   uint32_t lo = 0xFFFFFFFFu, hi = 0;
-  for_each<THREADS, 4>(r, 0, r.n_vec, [&](float z, int) {
+  for_each<THREADS, 4>(r, 0, r.n_vec, [&](float z) {
     const double X = x_of(z, c);
     if (X < kFar && (int)X == b) {
       const uint32_t k = key_of(z);
@@ -316,7 +316,7 @@ __device__ __noinline__ Place refine(Row<F32> r, Lds& s, Scale c, int b, Target 
       s.sub.num[i] = 0;
     }
     __syncthreads();
-    for_each<THREADS, 4>(r, 0, r.n_vec, [&](float z, int) {
+    for_each<THREADS, 4>(r, 0, r.n_vec, [&](float z) {
       const double X = x_of(z, c);
       const uint32_t k = key_of(z);
       if (X < kFar && (int)X == b && k >= lo && k <= hi) {
@@ -502,7 +502,8 @@ __device__ __forceinline__ Top top_part(const Row<F32>& r, int v0, int v1) {
       }
       if (lo == -INFINITY && v < v1) {
 #pragma unroll
-        for (int e = 0; e < E; ++e) t.masked += z[e] == -INFINITY && v * E + e < r.V;
+        for (int e = 0; e < E; ++e)      // (not those past the row's end)
+          t.masked += z[e] == -INFINITY && (uint32_t)v * E + e < (uint32_t)r.V;
       }
     }
   }
@@ -639,7 +640,7 @@ __device__ __forceinline__ Place resolve_all(const Cuts& x, uint32_t* kept, doub
   return resolve(Target{kExceed, 0, x.u * *M});
 }
 
-// A list of at most 64 tokens, one per lane: every wave sorts and resolves it for itself.
+// A list of at most 64 tokens, one per lane of the first wave.
 __device__ __forceinline__ Place resolve_short(Lds& s, const Scale& c, const Cuts& x,
                                                const Wanted& want, int n_list, uint32_t* kept,
                                                double* M) {

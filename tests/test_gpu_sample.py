@@ -250,3 +250,26 @@ def test_graph_and_streams(lg):
     torch.cuda.synchronize()
     for a, b in zip(got, ref):
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_the_longest_rows(lg):
+    """2^31 - 1 tokens: a few live ones at both ends, and all equal."""
+    V = (1 << 31) - 1
+    buf = torch.full((1, V + 1), float("nan"), dtype=torch.bfloat16, device="cuda")
+    z = buf[:, :V]
+    z.fill_(-float("inf"))
+    at = [0, 5, 1 << 30, V - 2, V - 1]
+    live = torch.tensor([1.0, 2.0, 3.0, 2.5, 0.5])
+    for i, x in zip(at, live.tolist()):
+        z[0, i] = x
+    for u in (0.0, 0.45, 0.7, 0.9, 0.9999):
+        for kw in (dict(), dict(top_k=3), dict(min_p=0.3)):
+            got = lg.sample_tokens(z, torch.tensor([u], device="cuda"), **kw)
+            ref = osample.row(live.double().numpy(), float(np.float32(u)),
+                              **{k: f32(v) if k != "top_k" else v for k, v in kw.items()})
+            assert got.token.item() == at[ref[0]] and got.kept.item() == ref[3]
+            assert abs(got.logp.item() - ref[1]) <= U * abs(ref[1]) + 1e-7
+            assert abs(got.logq.item() - ref[2]) <= U * abs(ref[2]) + 1e-7
+    z.fill_(2.0)
+    got = lg.sample_tokens(z, torch.tensor([0.75], device="cuda"))
+    assert got.token.item() == 3 * V // 4 and got.kept.item() == V
