@@ -243,10 +243,13 @@ def test_linear_empty_and_sizes(L):
     assert L.logra_linear_backward_act_ws_bytes(-1, 8) == 0
     assert L.logra_linear_backward_act_ws_bytes(8, 0) == 0
     assert L.logra_linear_backward_act_ws_bytes(8192, 4096) % 256 == 0
+    # few rows are added up by one launch, without scratch (which is then not looked at)
+    assert L.logra_linear_backward_act_ws_bytes(1000, 512) == 0
+    assert L.logra_linear_backward_act_ws_bytes(2000, 512) > 0
 
 
 def _act(L, **kw):
-    a = dict(d_out=A, d_out_type=0, ldd=512, pre=B, ldp=512, act=2, T=1000, d=512, dY=C, ldy=512,
+    a = dict(d_out=A, d_out_type=0, ldd=512, pre=B, ldp=512, act=2, T=2000, d=512, dY=C, ldy=512,
              d_bias=D, ws=W, ws_bytes=1 << 30, s=None)
     a.update(kw)
     return L.logra_linear_backward_act(*a.values())
