@@ -576,7 +576,7 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs g, TileGrid t) {
 // eight waves pieces of K; each lane reads W straight into the operand (16 bytes of one
 // row; the second load of a pair takes the other half of its 128-byte line), eight loads
 // in flight, and X likewise from the caches.  The waves' sums meet in LDS.
-// 1 x 4096 to 4096: 4.0 us (weights that the caches hold), 7 from HBM.
+// 1 x 4096 to 4096: 4.0 us (weights that the caches hold), 8.6 from HBM in a row of calls.
 constexpr int kFewWaves = 8;
 
 __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(GemmArgs g) {

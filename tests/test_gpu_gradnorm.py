@@ -203,3 +203,15 @@ def test_clip_past_the_caches(lg, gt, ot):
     assert abs(norm - ref) <= 1.001 * U * ref
     lg.grad_clip(b, torch.tensor([0.375], device="cuda"))
     assert all(torch.equal(x, w) for x, w in zip(gs if ot is None else outs, want))
+
+
+def test_handle_keeps_the_storage(lg):
+    """Gradients that the caller drops (or gives other storage) are still the handle's."""
+    gs = tensors([100_003, 77], [F32, BF], seed=12)
+    ref = onorm.norm([f64(g) for g in gs])[0]
+    b = lg.grad_norm_bind(gs)
+    gs[0].data = torch.zeros(5, device="cuda")
+    del gs
+    other = [torch.full((100_003,), 9.0, device="cuda") for _ in range(4)]
+    assert near(lg.grad_norm(b).norm, ref)
+    del other
