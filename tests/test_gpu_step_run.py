@@ -304,3 +304,57 @@ def test_two_streams_at_once(lg):
         for s, ref in zip(steps, refs):
             for i, (a, b) in enumerate(zip(s.results(), ref)):
                 assert same_bits(a, b), (rep, i)
+
+
+def test_binding_refuses(lg):
+    X, W = torch.zeros(64, 128, dtype=BF, device="cuda"), torch.zeros(96, 128, dtype=BF, device="cuda")
+    u, f = torch.zeros(64, device="cuda"), torch.zeros(96, device="cuda")
+    err = lg._lib.LograError
+    for kind, call in (
+            (err, lambda: lg.linear(X, W[:, :128].contiguous(), out=X[:, :96])),    # over its input
+            (err, lambda: lg.linear(X[:1].expand(64, 128), W)),
+            (ValueError, lambda: lg.linear(X.t(), W)),
+            (ValueError, lambda: lg.linear(X, W[:, :64])),
+            (ValueError, lambda: lg.linear(X, W, bias=f[:64])),
+            (ValueError, lambda: lg.linear(X, W, act="tanh")),
+            (ValueError, lambda: lg.linear(X, W, out_dtype=torch.float16)),
+            (ValueError, lambda: lg.linear(X.float(), W)),
+            (ValueError, lambda: lg.linear(X, W, residual=X)),
+            (ValueError, lambda: lg.linear_backward_act(X, act="relu")),
+            (ValueError, lambda: lg.linear_backward_act(X, pre=X)),
+            (ValueError, lambda: lg.linear_backward_input(X, W)),
+            (ValueError, lambda: lg.linear_backward_weight(X, W)),
+            (ValueError, lambda: lg.linear_backward_weight(X, X, accumulate=True)),
+            (ValueError, lambda: lg.linear_backward_weight(X, X, dW=torch.zeros_like(X), accumulate=True)),
+            (ValueError, lambda: lg.sample_tokens(X, u[:63])),
+            (ValueError, lambda: lg.sample_tokens(X.half(), u)),
+            (ValueError, lambda: lg.sample_tokens(X, u, top_k=-1)),
+            (ValueError, lambda: lg.sample_tokens(X, u, top_k=u)),
+            (ValueError, lambda: lg.sample_tokens(X, u, tau=u[:3])),
+            (err, lambda: lg.sample_tokens(X, u, tau=0)),
+            (err, lambda: lg.sample_tokens(X, u, top_p=1.5)),
+            (ValueError, lambda: lg.grad_norm_bind([X, X])),
+            (ValueError, lambda: lg.grad_norm_bind([X.t()])),
+            (ValueError, lambda: lg.grad_norm_bind([X], out=[f])),
+            (ValueError, lambda: lg.grad_norm(lg.grad_norm_bind([X]), norm_type=1)),
+            (ValueError, lambda: lg.grad_norm(lg.grad_norm_bind([X]), grad_scale=u)),
+            (ValueError, lambda: lg.grad_clip(lg.grad_norm_bind([X]), u))):
+        with pytest.raises(kind):
+            call()
+    assert not X.any() and not W.any()
+
+
+def test_the_same_tensor_twice(lg):
+    """One tensor as two inputs, and a batch without rows."""
+    X = torch.randint(-2, 3, (64, 128), device="cuda").to(BF)
+    W = torch.randint(-2, 3, (128, 128), device="cuda").to(BF)
+    x, w = f64(X), f64(W)
+    bf16 = lambda a: torch.from_numpy(a).to(BF)
+    assert torch.equal(lg.linear(X, W, residual=X).cpu(), bf16(x @ w.T + x))
+    assert torch.equal(lg.linear(W, W).cpu(), bf16(w @ w.T))
+    assert torch.equal(lg.linear_backward_input(X, W, residual=X).cpu(), bf16(x @ w + x))
+    assert np.array_equal(f64(lg.linear_backward_weight(X, X)), x.T @ x)
+    none = torch.empty(0, 128, dtype=BF, device="cuda")
+    assert lg.linear(none, W).shape == (0, 128) and lg.linear_backward_act(none).shape == (0, 128)
+    assert lg.sample_tokens(none, torch.empty(0, device="cuda")).token.shape == (0,)
+    assert not lg.linear_backward_weight(none, none).any()
