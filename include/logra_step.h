@@ -143,7 +143,8 @@ int logra_grad_clip(const void* table, const void* table_dev, const float* scale
 
 /* ------------------------------------------------------------------ layer product */
 
-/* Activations. */
+/* Activations, as these formulas give them: +inf stays +inf, -inf is 0 under relu and
+ * NaN (-inf times 0) under the others, NaN stays NaN. */
 #define LOGRA_ACT_NONE 0
 #define LOGRA_ACT_RELU 1        /* max(x, 0) */
 #define LOGRA_ACT_SILU 2        /* x / (1 + e^-x) */

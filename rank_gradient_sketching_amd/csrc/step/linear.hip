@@ -64,7 +64,8 @@ __device__ __forceinline__ float activate(float x) {
   if constexpr (ACT == kActGelu) {
     float e;
     const float q = tail(x, &e);
-    return fmaf(-fabsf(x), q, x > 0.f || x != x ? x : 0.f);
+    // (from 100 on q is 0: clamped there, +inf is not inf times 0)
+    return fmaf(x > 0.f ? -fminf(x, 100.f) : x, q, x > 0.f || x != x ? x : 0.f);
   }
   if constexpr (ACT == kActGeluTanh) return x * sigmoid(kGeluA * fmaf(kGeluB * x * x, x, x));
   return x;
