@@ -303,6 +303,8 @@ def linear_backward_act(d_out, pre=None, act=None, dY=None, d_bias=None, ws=None
     else:
         dY, ldy = _rows_out(T, d, torch.bfloat16, d_out)
         y_ptr = dY.data_ptr()
+    if T == 0 and d_bias is None:       # (no address, so no output that the library could see)
+        return dY
     need = 0 if d_bias is None else linear_backward_act_ws_bytes(T, d)
     ws_ptr, ws_n, ws = _workspace(ws, need, d_out)
     _call("logra_linear_backward_act", dev, d_out.data_ptr(), _TYPES[d_out.dtype], ldd, p_ptr, ldp,
