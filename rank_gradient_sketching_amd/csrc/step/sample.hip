@@ -173,6 +173,7 @@ struct Lds {
     u64 wave_q[kMaxWaves];
   };
   uint32_t wave_u[kMaxWaves];
+  double wave_end[kMaxWaves];
   double at_mass;
   uint32_t at_rank, at_key, n_list;
   int at_index;
@@ -900,13 +901,28 @@ __device__ __noinline__ Drawn pick(Row<F32> r, Lds& s, Scale c, Settings g, Coun
         n0 += s.wave_u[w];
       }
     d0 += w_d;
+    // d0 is rounded along another path than the sum that the threads before end with, so a
+    // bin without tokens would lie a rounding above (or below) the one before it, and a
+    // target in between would find no token there.  A thread therefore starts from the
+    // largest end of those before it: the masses never fall, and rise at tokens only.
+    double end = ns != 0 ? d0 + ds : 0.0;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) end = fmax(end, __shfl_up(end, off));
+    double start = __shfl_up(end, 1);
+    start = threadIdx.x % 64 ? start : 0.0;
+    if (threadIdx.x % 64 == 63) s.wave_end[threadIdx.x / 64] = end;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < THREADS / 64; ++w)
+      if (w < (int)(threadIdx.x / 64)) start = fmax(start, s.wave_end[w]);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      s.cum[threadIdx.x * kPer + i] = d0 + d[i];
+      d[i] = n[i] != 0 ? fmax(start, d0 + d[i]) : start;
+      s.cum[threadIdx.x * kPer + i] = d[i];
       s.num[threadIdx.x * kPer + i] = n0 + n[i];
     }
     if (((int)threadIdx.x + 1) * kPer % 64 == 0) {
-      s.group_cum[threadIdx.x * kPer / 64] = d0 + d[kPer - 1];
+      s.group_cum[threadIdx.x * kPer / 64] = d[kPer - 1];
       s.group_num[threadIdx.x * kPer / 64] = n0 + n[kPer - 1];
     }
     if (threadIdx.x == 0) s.n_list = 0;
