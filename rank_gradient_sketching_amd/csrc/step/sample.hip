@@ -173,7 +173,6 @@ struct Lds {
     u64 wave_q[kMaxWaves];
   };
   uint32_t wave_u[kMaxWaves];
-  double wave_end[kMaxWaves];
   double at_mass;
   uint32_t at_rank, at_key, n_list;
   int at_index;
@@ -883,16 +882,25 @@ __device__ __noinline__ Drawn pick(Row<F32> r, Lds& s, Scale c, Settings g, Coun
         n0 += o_n;
       }
     }
-    if (threadIdx.x % 64 == 63) {
-      s.wave_d[threadIdx.x / 64] = d0;
-      s.wave_u[threadIdx.x / 64] = n0;
-    }
-    __syncthreads();
-    // (what lies before this thread: its wave's part without its own, and the waves')
+    // The wave's part before this thread.  It is rounded along another path than the sum
+    // that the threads before end with, so a bin without tokens would lie a rounding above
+    // (or below) the one before it, and a target in between would find no token there.  A
+    // thread therefore starts from the largest end of those before it: the masses never
+    // fall, and rise at tokens only.  (Adding the waves before keeps equal ones equal.)
     const double up_d = __shfl_up(d0, 1);
     const uint32_t up_n = __shfl_up(n0, 1);
     d0 = threadIdx.x % 64 ? up_d : 0.0;
+    double end = ns != 0 ? d0 + ds : 0.0;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) end = fmax(end, __shfl_up(end, off));
+    if (threadIdx.x % 64 == 63) {
+      s.wave_d[threadIdx.x / 64] = end;
+      s.wave_u[threadIdx.x / 64] = n0;
+    }
+    const double up_end = __shfl_up(end, 1);
+    const double start = threadIdx.x % 64 ? up_end : 0.0;
     n0 = threadIdx.x % 64 ? up_n : 0u;
+    __syncthreads();
     double w_d = 0;
 #pragma unroll
     for (int w = 0; w < THREADS / 64; ++w)
@@ -900,24 +908,9 @@ __device__ __noinline__ Drawn pick(Row<F32> r, Lds& s, Scale c, Settings g, Coun
         w_d += s.wave_d[w];
         n0 += s.wave_u[w];
       }
-    d0 += w_d;
-    // d0 is rounded along another path than the sum that the threads before end with, so a
-    // bin without tokens would lie a rounding above (or below) the one before it, and a
-    // target in between would find no token there.  A thread therefore starts from the
-    // largest end of those before it: the masses never fall, and rise at tokens only.
-    double end = ns != 0 ? d0 + ds : 0.0;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) end = fmax(end, __shfl_up(end, off));
-    double start = __shfl_up(end, 1);
-    start = threadIdx.x % 64 ? start : 0.0;
-    if (threadIdx.x % 64 == 63) s.wave_end[threadIdx.x / 64] = end;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < THREADS / 64; ++w)
-      if (w < (int)(threadIdx.x / 64)) start = fmax(start, s.wave_end[w]);
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      d[i] = n[i] != 0 ? fmax(start, d0 + d[i]) : start;
+      d[i] = w_d + (n[i] != 0 ? fmax(start, d0 + d[i]) : start);
       s.cum[threadIdx.x * kPer + i] = d[i];
       s.num[threadIdx.x * kPer + i] = n0 + n[i];
     }
