@@ -547,10 +547,7 @@ __device__ __forceinline__ uint32_t bin_part(const Row<F32>& r, int v0, int v1, 
 #pragma unroll
       for (int e = 0; e < E; ++e) X[e] = x_of(z[e], c);
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        b[e] = (int)X[e];
-        b[e] = (uint32_t)b[e] < (uint32_t)kBins ? b[e] : spare;
-      }
+      for (int e = 0; e < E; ++e) b[e] = X[e] < kFar ? (int)X[e] : spare;
 #pragma unroll
       for (int e = 0; e < E; ++e) w[e] = weight_of(X[e], c);
 #pragma unroll
