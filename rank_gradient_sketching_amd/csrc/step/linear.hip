@@ -890,7 +890,7 @@ ActGrid make_act_grid(int64_t T, int64_t d, bool sums) {
 
 template <int ACT>
 void launch_act(const ActGradArgs& a, const ActGrid& g, hipStream_t s) {
-  const int cols = g.narrow ? kNarrowCols : kStripCols;
+  const int64_t cols = g.narrow ? kNarrowCols : kStripCols;     // (d and it pass 2^31 together)
   const dim3 grid((unsigned)((a.d + cols - 1) / cols), (unsigned)g.chunks);
   const dim3 block(g.narrow ? kNarrowThreads : 256);
   constexpr int kN = kNarrowCols / 8, kS = kStripCols / 8;
@@ -953,8 +953,8 @@ hipError_t launch_act_grad(const ActGradArgs& a, char* ws, hipStream_t s) {
     default: launch_act<kActGeluTanh>(a, g, s);
   }
   if (a.d_bias != nullptr && g.chunks > 1)
-    hipLaunchKernelGGL(bias_join_kernel, dim3((unsigned)((a.d + 63) / 64)), dim3(256), 0, s,
-                       g.partial, g.chunks, a.d, a.d_bias);
+    hipLaunchKernelGGL(bias_join_kernel, dim3((unsigned)(((int64_t)a.d + 63) / 64)), dim3(256), 0,
+                       s, g.partial, g.chunks, a.d, a.d_bias);
   return hipGetLastError();
 }
 

@@ -98,3 +98,17 @@ def test_far_side_keeps_its_digits(lg, act):
     want = {"gelu": lambda: x * 0.5 * erfc(-x / np.sqrt(2)), "silu": lambda: x * expit(x),
             "gelu_tanh": lambda: x * expit(2 * np.sqrt(2 / np.pi) * (x + 0.044715 * x ** 3))}[act]()
     assert np.all(np.abs(got - want) <= units(x) * U * np.abs(want))
+
+
+def test_activation_gradient_of_the_widest_row(lg):
+    """One row of 2^31 - 1 columns: slopes of 0 and 1, so all values are exact."""
+    d = (1 << 31) - 1
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    x = torch.randint(-3, 4, (1, d + 1), device="cuda", generator=g, dtype=torch.int8).to(BF)[:, :d]
+    d_bias = torch.full((d,), NAN, device="cuda")
+    dY = lg.linear_backward_act(x, x, "relu", d_bias=d_bias)
+    for a in range(0, d, 1 << 28):
+        want = x[0, a:a + (1 << 28)].clamp(min=0)
+        assert torch.equal(dY[0, a:a + (1 << 28)], want)
+        assert torch.equal(d_bias[a:a + (1 << 28)], want.float())
