@@ -46,6 +46,7 @@ logra::GradNormArgs grad_args(const logra::GradTable& t, const void* table_dev) 
   a.n = t.n;
   a.groups = t.groups;
   a.loops = t.loops;
+  a.large = t.large != 0;
   return a;
 }
 

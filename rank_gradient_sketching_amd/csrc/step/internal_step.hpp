@@ -45,16 +45,16 @@ struct GradTable {
   uint64_t bytes;
   int32_t n, groups;
   int32_t loops;      // steps of a work-group
-  int32_t pad;
+  int32_t large;      // more gradients than are worth keeping in the caches
 };
-// Fills in the head's loops and groups, the items' vec and the first work-groups;
+// Fills in the head's loops, groups and large, the items' vec and the first work-groups;
 // false where the work-groups do not fit a launch.
 bool grad_lay_out(GradTable* head, GradItem* items, int32_t* first);
 struct GradNormArgs {
   const GradItem* items;     // device
   const int32_t* first;      // device, n + 1
   int32_t n, groups, loops;
-  bool inf_norm;
+  bool large, inf_norm;
   double max_norm;
   const float* grad_scale;
   float* norm;

@@ -282,14 +282,22 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(const GradItem* __restri
   }
 }
 
+// Past the caches from 128 MiB of gradients: norm and clip of 233570304 bf16 entries 250
+// us (268 through them), 4 x 4096 x 4096 fp32 in place 152 (158); 168 x 13001 bf16, which
+// the caches hold, 14.2 (11.1), 5000 x 1536 fp32 in place 33.9 (32.5).
+constexpr int64_t kLargeBytes = (int64_t)128 << 20;
+
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 }  // namespace
 
 bool grad_lay_out(GradTable* head, GradItem* items, int32_t* first) {
-  int64_t steps = 0;
-  for (int i = 0; i < head->n; ++i)
+  int64_t steps = 0, bytes = 0;
+  for (int i = 0; i < head->n; ++i) {
     steps += (items[i].n * elem(items[i].g_f32) + kBytes - 1) / kBytes;
+    bytes += items[i].n * elem(items[i].g_f32);
+  }
+  head->large = bytes >= kLargeBytes;
   const int64_t loops = (steps + kGroups - 1) / kGroups;
   head->loops = (int32_t)(loops < 1 ? 1 : loops > (1 << 20) ? 1 << 20 : loops);
   int64_t groups = 0;
@@ -323,12 +331,8 @@ hipError_t launch_grad_norm(const GradNormArgs& a, double* partial, hipStream_t 
   return hipGetLastError();
 }
 
-// Past the caches from 128 MiB of gradients: norm and clip of 233570304 bf16 entries 250
-// us (268 through them), 4 x 4096 x 4096 fp32 in place 152 (158); 168 x 13001 bf16, which
-// the caches hold, 14.2 (11.1).
 hipError_t launch_grad_clip(const GradNormArgs& a, const float* scale, hipStream_t s) {
-  const bool past = (int64_t)a.groups * a.loops * kBytes >= (int64_t)128 << 20;
-  hipLaunchKernelGGL(past ? clip_kernel<true> : clip_kernel<false>, dim3((unsigned)a.groups),
+  hipLaunchKernelGGL(a.large ? clip_kernel<true> : clip_kernel<false>, dim3((unsigned)a.groups),
                      dim3(kThreads), 0, s, a.items, a.first, a.n, a.loops, scale);
   return hipGetLastError();
 }

@@ -21,7 +21,8 @@ Launch = namedtuple("Launch", "name grid block")
 
 def follow(calls, folder):
     """[(status, [Launch, ...]), ...] of calls [(entry point, [arguments]), ...]; folder:
-    where the stand-in is built."""
+    where the stand-in is built.  An argument {"grads": [[entries, type], ...]} is the table
+    that logra_grad_table makes of such tensors."""
     fake = os.path.join(str(folder), "fake_hip.so")
     if not os.path.exists(fake):
         subprocess.run(["gcc", "-std=c11", "-O1", "-Wall", "-Wextra", "-Werror", "-shared", "-fPIC",
@@ -31,6 +32,17 @@ def follow(calls, folder):
     assert res.returncode == 0, res.stdout[-2000:] + res.stderr[-4000:]
     return [(st, [Launch(n, tuple(g), tuple(b)) for n, g, b in ls]) for st, ls in
             json.loads(res.stdout)]
+
+
+def _table(loader, lib, grads):
+    items = (loader.GradItem * len(grads))()
+    for q, (n, kind) in zip(items, grads):
+        q.g, q.n, q.g_type = 1 << 40, n, kind
+    size = lib.logra_grad_table_bytes(len(grads))
+    table = (ctypes.c_uint64 * (size // 8))()
+    if lib.logra_grad_table(len(grads), items, table, size) != 0:
+        sys.exit("the table was refused")
+    return table
 
 
 def _child(fake):
@@ -48,6 +60,8 @@ def _child(fake):
         sys.exit("the library's kernels are not registered with the stand-in")
     out = []
     for name, args in json.load(sys.stdin):
+        tables = [_table(loader, lib, x["grads"]) if isinstance(x, dict) else None for x in args]
+        args = [x if t is None else ctypes.addressof(t) for x, t in zip(args, tables)]
         stand_in.fake_hip_clear()
         status = getattr(lib, name)(*args)
         n = stand_in.fake_hip_launches()

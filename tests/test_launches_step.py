@@ -84,3 +84,23 @@ def test_many_rows_of_draws(folder):
     for (_, args), (st, launches) in zip(calls, follow(calls, folder)):
         assert st == 0 and sum(x.grid[0] for x in launches) == args[2]
         assert all(x.grid[0] <= 1 << 22 for x in launches)
+
+
+BF16, F32 = 0, 1
+MIB = 1 << 20
+
+
+@pytest.mark.parametrize("grads,past", [
+    ([[100, F32]] * 4096, False),                       # 1.6 MB: a work-group each, but few bytes
+    ([[1536, F32]] * 5000, False),
+    ([[1, BF16]] * 20000, False),
+    ([[16 * MIB, BF16], [24 * MIB - 1, F32]], False),   # one entry short of 128 MiB
+    ([[16 * MIB, BF16], [24 * MIB, F32]], True),
+    ([[64 * MIB - 1, BF16]], False),
+    ([[64 * MIB, BF16]], True),
+    ([[4 * MIB, F32]] * 8 + [[0, F32]] * 9, True),
+    ([[152064 * 1536, BF16]], True),
+], ids=lambda x: str(x) if isinstance(x, bool) else f"{len(x)}x{x[0]}")
+def test_clip_passes_the_caches_from_128_mib(folder, grads, past):
+    (st, (clip,)), = follow([("logra_grad_clip", [{"grads": grads}, W, C, None])], folder)
+    assert st == 0 and f"clip_kernelILb{int(past)}E" in clip.name
