@@ -3,6 +3,7 @@
 import pytest
 
 from launches import follow
+from linear_kernel_shapes import FORMS, SHAPES, form_of, has
 
 A, B, C, D, E, F, G, W = (0x10000000000000 * i for i in range(1, 9))   # 2^52 bytes apart
 TOP = (1 << 31) - 1
@@ -104,3 +105,35 @@ MIB = 1 << 20
 def test_clip_passes_the_caches_from_128_mib(folder, grads, past):
     (st, (clip,)), = follow([("logra_grad_clip", [{"grads": grads}, W, C, None])], folder)
     assert st == 0 and f"clip_kernelILb{int(past)}E" in clip.name
+
+
+def test_products_reach_the_kernels_that_are_tested(folder):
+    """Each shape of linear_kernel_shapes.py, in each form, goes to the kernel that it is there
+    for; all of the library's product kernels are among them, split and whole."""
+    cases = [(s, f) for s in SHAPES for f in FORMS if has(s, f)]
+    calls = []
+    for s, form in cases:
+        T, d, k = form_of(s, form)
+        ld, lk = up(d, 8), up(k, 8)
+        calls.append({
+            "forward": ("logra_linear", [A, lk, B, lk, T, d, k, None, 0, 0, None, 0, C, 1, ld, None,
+                                         0, W, MANY, None]),
+            "input": ("logra_linear_backward_input", [A, ld, B, lk, T, d, k, None, 0, C, lk, W, MANY,
+                                                      None]),
+            "weight": ("logra_linear_backward_weight", [A, ld, B, lk, T, d, k, 0, C, 1, lk, W, MANY,
+                                                        None])}[form])
+    for (s, form), (st, (first, *join)) in zip(cases, follow(calls, folder)):
+        bits = {"forward": "Lb0ELb0E", "input": "Lb0ELb1E", "weight": "Lb1ELb1E"}[form]
+        if s.kernel == "few":
+            want = "few_rows_kernelE"
+        elif s.kernel.startswith("64"):
+            want = "tile_kernelILi%sELi%sE" % tuple(s.kernel.split("x"))
+            assert first.name.split("EE")[0].endswith(bits + f"Lb{int(s.once)}"), (s, form, first)
+        else:
+            want = "big_kernelILi%sE%sE" % (s.kernel.split("x")[1], bits)
+        assert st == 0 and want in first.name, (s, form, first)
+        assert [("join_kernel" in x.name) for x in join] == [True] * s.split, (s, form, join)
+    kinds = {(s.kernel, s.once, s.split) for s in SHAPES}
+    assert kinds == {("few", False, False)} | {
+        (t, o, p) for t in ("64x64", "64x128", "256x128", "256x256") for p in (False, True)
+        for o in ((False, True) if t.startswith("64") else (False,))}
