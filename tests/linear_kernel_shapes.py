@@ -26,6 +26,15 @@ SHAPES = [
     Shape("256x256", False, False, 8190, 4090, 1101),
     Shape("256x256", False, True, 1301, 2501, 8203),
 ]
+
+# Activation gradients with a bias gradient: rows, columns, and whether strips of 256 columns
+# (else 16) are added up, and in how many chunks of rows.
+BIAS_SHAPES = [
+    (1024, 777, False, 1), (1, 10240, False, 1), (1023, 10239, False, 1),
+    (1025, 777, True, 129), (2050, 4099, True, 52), (5000, 10249, True, 25), (40, 10249, True, 5),
+    (9, 10241, True, 2), (8, 10241, True, 1), (1, 70001, True, 1), (4100, 36, True, 513),
+    (8200, 257, True, 342), (130, 300001, True, 1),
+]
 FORMS = ("forward", "input", "weight")
 
 

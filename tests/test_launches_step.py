@@ -3,7 +3,7 @@
 import pytest
 
 from launches import follow
-from linear_kernel_shapes import FORMS, SHAPES, form_of, has
+from linear_kernel_shapes import BIAS_SHAPES, FORMS, SHAPES, form_of, has
 
 A, B, C, D, E, F, G, W = (0x10000000000000 * i for i in range(1, 9))   # 2^52 bytes apart
 TOP = (1 << 31) - 1
@@ -137,3 +137,14 @@ def test_products_reach_the_kernels_that_are_tested(folder):
     assert kinds == {("few", False, False)} | {
         (t, o, p) for t in ("64x64", "64x128", "256x128", "256x256") for p in (False, True)
         for o in ((False, True) if t.startswith("64") else (False,))}
+
+
+def test_bias_gradients_reach_the_kernels_that_are_tested(folder):
+    for T, d, strips, chunks in BIAS_SHAPES:
+        for kind in (BF16, F32):
+            (st, (first, *join)), = follow([act(T, d, act=2, d_type=kind)], folder)
+            cols, threads = (256, 256) if strips else (16, 512)
+            assert st == 0 and (f"act_grad_kernelILi2ELb{kind}ELi{cols // 8}ELi{threads}E"
+                                in first.name), (T, d)
+            assert first.grid == (up(d, cols) // cols, chunks, 1), (T, d, first)
+            assert ["bias_join_kernel" in x.name for x in join] == [True] * (chunks > 1)
