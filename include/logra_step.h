@@ -45,9 +45,10 @@ size_t logra_sample_tokens_ws_bytes(int64_t n_tok, int64_t vocab);
  *   logp[t] = log p_token: what logra_token_logprob gives for that target
  *   logq[t] = log (p_token / M): the probability it was drawn with
  *   kept[t] = K
- * Masses are exact to about 2^-44 of each (fp64 exponentials, added as integers, so
- * in no order), so that a draw differs from one in exact arithmetic only where u M
- * lies that near to a border.
+ * Masses are exact to about 2^-44 of each up to vocabularies of 2^18, to vocab 2^-62
+ * past that (2^-31 at 2^31 tokens): fp64 exponentials, added as integers, so in no order, of
+ * as many bits as let a sum of vocab of them fit.  A draw differs from one in exact
+ * arithmetic only where u M lies that near to a border.
  *
  * A row with u[t] outside [0, 1) (an ended sequence: -1) is left out: token -1,
  * logp, logq and kept 0, its logits not read.  A row with a NaN or +inf logit,
@@ -137,6 +138,7 @@ int logra_grad_norm(const void* table, const void* table_dev, int kind, double m
  * logra_grad_norm left it): out = g scale in fp32, rounded to out's type (bf16: to
  * nearest even); in place where out is NULL, with nothing to do where scale is 1.
  * For gradients that no optimizer scales itself (logra_sketch_update, logra_merge).
+ * scale lies in nothing that is written (not checked).
  * Returns LOGRA_OK, LOGRA_EINVAL or LOGRA_EHIP.
  */
 int logra_grad_clip(const void* table, const void* table_dev, const float* scale, hipStream_t s);

@@ -13,9 +13,9 @@
 //
 // Bound: the matrix cores' power for large products (the clock falls to 1.5 - 1.9 GHz
 // under them; a loop of nothing but 32x32x16 products of random numbers reaches 1830
-// TFLOP/s, 16x16x32 ones 1700): 8192 x 4096 x 4096 takes 200, 198 and 199 us in the three
-// forms (1380 TFLOP/s; the library's products 175 - 200, 201 and 230); the weights' HBM
-// bytes for few rows (64 x 1536 to 152064 fp32 results: 102 us, 5.0 TB/s).
+// TFLOP/s, 16x16x32 ones 1700): 8192 x 4096 x 4096 takes 218, 210 and 209 us in the three
+// forms (1260 to 1315 TFLOP/s; the library's products 179, 212 and 232); the weights' HBM
+// bytes for few rows (64 x 1536 to 152064 fp32 results: 98 us, 5.2 TB/s).
 #include <math.h>
 
 #include "common.hpp"
@@ -476,8 +476,8 @@ __global__ __launch_bounds__(kBigThreads) void big_kernel(GemmArgs g, TileGrid t
 // step's copies are issued STAGES - 1 steps ahead and waited for by count, so that
 // the memory's latency is paid once and not in every step.
 // 64 x 64 with four stages and 64 x 128 with three leave room for two work-groups on a
-// CU (64 x 128 with four stages has a CU to itself: 200 x 1536 to 8960 21 us, with
-// three 18; 128 x 128 is no faster than 64 x 128 anywhere).  ONCE: results of one tile of
+// CU (64 x 128 with four stages has a CU to itself: 200 x 1536 to 8960 32 us, with
+// three 21; 128 x 128 is no faster than 64 x 128 anywhere).  ONCE: results of one tile of
 // rows, whose weights no other work-group reads, copied past the caches (64 x 1536 to
 // 152064 109 -> 102 us, 32 x 4096 to 32000 57 -> 51; few_rows_kernel lost by it).
 template <int BM, int BN, int WM, int WN, int STAGES, bool AK, bool BK, bool ONCE>
@@ -577,7 +577,7 @@ __global__ __launch_bounds__(256) void join_kernel(GemmArgs g, TileGrid t) {
 // eight waves pieces of K; each lane reads W straight into the operand (16 bytes of one
 // row; the second load of a pair takes the other half of its 128-byte line), eight loads
 // in flight, and X likewise from the caches.  The waves' sums meet in LDS.
-// 1 x 4096 to 4096: 4.0 us (weights that the caches hold), 8.6 from HBM in a row of calls.
+// 1 x 4096 to 4096: 4.0 us (weights that the caches hold), 9.7 from HBM in a row of calls.
 constexpr int kFewWaves = 8;
 
 __global__ __launch_bounds__(kFewWaves * 64) void few_rows_kernel(GemmArgs g) {

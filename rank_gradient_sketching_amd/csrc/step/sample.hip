@@ -26,12 +26,12 @@
 // Bound.  A row is read twice or three times (maximum, bins, gathered list), the later
 // times out of the caches, and what each logit costs in between (an fp64 product, the
 // polynomial, two LDS atomics: some 40 issue slots a wave and logit) is far more than
-// its two bytes.  512 x 152064 bf16 takes 150 us, of them 25 the maximum, 40 the bins,
-// 7 their scan, 25 the gathering and up to 15 the resolving; read once at the rate of a
-// copy it would take 30.  A work-group of 512 threads holds 49 KB of bins, so two
+// its two bytes.  512 x 152064 bf16 takes 147 us: 25 the maximum, 40 the bins, 7 their
+// scan, 25 the gathering and up to 15 the resolving; the other 35 are not attributed.  Read
+// once at 7.2 TB/s it would take 22.  A work-group of 512 threads holds 49 KB of bins, so two
 // share a CU and one's barriers hide behind the other's logits; four of 256 threads do
 // not fit, one of 1024 took 184 us.  Few rows leave CUs idle, so they are cut into
-// pieces: 8 x 152064 takes 39 us (6 + 9 + 24: maximum, bins, pick) against 57 with a
+// pieces: 8 x 152064 takes 39 us (6 + 9 + 25: maximum, bins, pick) against 57 with a
 // work-group per row; the pick's own gathering (9 us) and its loading and scanning of
 // the bins (8) are latency.
 #include <math.h>

@@ -122,7 +122,9 @@ def grad_norm_bind(grads, out=None):
     gradient with another's out.  The handle keeps the storage that the tensors
     have now: bind again after giving one other storage.  It copies a table to the
     GPU, so it is made outside a stream capture, and is kept until its calls have
-    run (a captured one: as long as its graph)."""
+    run (a captured one: as long as its graph).  It takes the host about 1.2 us a
+    tensor, so a program with many of them keeps its gradients' storage from step
+    to step (zero_grad(set_to_none=False)) and binds once."""
     grads = list(grads)
     n = len(grads)
     if n == 0:
