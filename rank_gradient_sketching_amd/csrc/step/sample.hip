@@ -887,7 +887,9 @@ __device__ __noinline__ Drawn pick(Row<F32> r, Lds& s, Scale c, Settings g, Coun
     const double up_d = __shfl_up(d0, 1);
     const uint32_t up_n = __shfl_up(n0, 1);
     d0 = threadIdx.x % 64 ? up_d : 0.0;
-    double end = ns != 0 ? d0 + ds : 0.0;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) d[i] += d0;
+    double end = ns != 0 ? d[kPer - 1] : 0.0;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) end = fmax(end, __shfl_up(end, off));
     if (threadIdx.x % 64 == 63) {
@@ -907,7 +909,7 @@ __device__ __noinline__ Drawn pick(Row<F32> r, Lds& s, Scale c, Settings g, Coun
       }
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
-      d[i] = w_d + (n[i] != 0 ? fmax(start, d0 + d[i]) : start);
+      d[i] = w_d + (n[i] != 0 ? fmax(start, d[i]) : start);
       s.cum[threadIdx.x * kPer + i] = d[i];
       s.num[threadIdx.x * kPer + i] = n0 + n[i];
     }
